@@ -32,7 +32,8 @@ STATUS = {0: "SDPA_OK", -1: "SDPA_ERR_INVALID_ARG", -2: "SDPA_ERR_UNSUPPORTED",
 # Every symbol include/sdpa.h declares.
 EXPORTS = ("sdpa_fwd", "sdpa_fwd_ex", "sdpa_fwd_strided", "sdpa_merge", "sdpa_select_path", "sdpa_fwd_host",
            "sdpa_fwd_split_kv_static", "sdpa_last_device_error", "sdpa_debug_checks", "sdpa_selftest_wait_timeout",
-           "sdpa_selftest_index_check", "sdpa_strerror", "sdpa_version")
+           "sdpa_selftest_index_check", "sdpa_strerror", "sdpa_version", "sdpa_cache_write", "sdpa_cache_read",
+           "sdpa_fwd_paged", "sdpa_fwd_paged_workspace")
 
 
 class SdpaError(RuntimeError):
@@ -49,6 +50,10 @@ class sdpa_mask_t(ctypes.Structure):
 class sdpa_strides_t(ctypes.Structure):
     _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("t", ctypes.c_int64)]
 
+
+from . import paged  # noqa: E402  (the paged cache operators)
+from .paged import (KVCache, PAGED_PATHS, cache_read, cache_write, sdpa_batch_t, sdpa_cache_read,  # noqa: E402,F401
+                    sdpa_cache_t, sdpa_cache_write, sdpa_fwd_paged, sdpa_fwd_paged_workspace, sdpa_paged, sdpa_rows_t)
 
 _lib = None
 _vp, _i32, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
@@ -81,6 +86,7 @@ def lib():
                      "sdpa_fwd_split_kv_static", "sdpa_last_device_error", "sdpa_selftest_wait_timeout",
                      "sdpa_selftest_index_check", "sdpa_debug_checks", "sdpa_version"):
             getattr(L, name).restype = _i32
+        paged.bind(L)
         _lib = L
     return _lib
 

@@ -261,6 +261,8 @@ int workspace_get(size_t cnt_bytes, size_t data_bytes, void** cnt, void** data, 
   return SDPA_OK;
 }
 
+int* error_word() { return error_word_ptr(); }
+
 int num_sms() {
   static int cached[kMaxDevices] = {0};
   int dev = 0;
@@ -577,7 +579,7 @@ extern "C" const char* sdpa_strerror(int status) {
     case SDPA_ERR_CUDA: return "CUDA error";
     case SDPA_ERR_TIMEOUT: return "device-side wait timed out";
     case SDPA_ERR_CAPACITY: return "request exceeds a fixed-size buffer";
-    case SDPA_ERR_DEVICE_INDEX: return "device-side index check failed (debug build)";
+    case SDPA_ERR_DEVICE_INDEX: return "device-side index check failed";
   }
   return "unknown status";
 }

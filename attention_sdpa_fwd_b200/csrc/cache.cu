@@ -1,0 +1,325 @@
+// Writing new keys and values into a paged cache, and reading sequences back.
+//
+// An 8-bit cache holds one f32 scale per (token, head) row of d elements:
+//   s = max(fl(amax / Q), 2^-30),  Q = 448 (e4m3) or 127 (int8)
+//   code = round_to_type(fl(x / s)), ties to even, saturated;  value = code * s
+// with fl the rounding to fp32 (IEEE division), so the codes are the same
+// wherever they are computed.  amax skips NaN elements; those become the NaN
+// code (e4m3) or 0 (int8).  The floor keeps every scale and its reciprocal a
+// normal number and bounds how far apart two scales of ordinary rows can be.
+//
+// Both are HBM-bound: each element is read once and written once.  A row is
+// held by a group of neighbouring lanes, 16 bytes of the wider side each, so
+// its amax is a few shuffles and nothing is staged; a warp keeps several rows
+// in flight to cover the latency of their loads.
+#include "paged.cuh"
+#include "pdl_launch.cuh"
+
+namespace sdpa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowsAhead = 4;  // rows a lane group has in flight
+
+// Sequence of packed row t: the last b with cu[b] <= t (0 if there is none),
+// searched by the whole warp, 32 boundaries at a time.
+__device__ __forceinline__ int find_seq(const int* cu, int B, int t, int lane) {
+  int lo = 0, n = B;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, i < n && __ldg(cu + lo + i) <= t);
+    const int k = max(0, __popc(le) - 1);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+template <typename T, typename C>
+__device__ __forceinline__ C encode(float x, float s);
+template <> __device__ __forceinline__ float encode<float, float>(float x, float) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 encode<__nv_bfloat16, __nv_bfloat16>(float x, float) {
+  return __float2bfloat16_rn(x);
+}
+__device__ __forceinline__ __nv_fp8_e4m3 to_e4m3(float x, float s) {
+  __nv_fp8_e4m3 r;
+  r.__x = __nv_cvt_float_to_fp8(__fdiv_rn(x, s), __NV_SATFINITE, __NV_E4M3);
+  return r;
+}
+__device__ __forceinline__ int8_t to_int8(float x, float s) {
+  const float y = rintf(__fdiv_rn(x, s));
+  return (int8_t)(int)fminf(fmaxf(y != y ? 0.f : y, -127.f), 127.f);
+}
+template <> __device__ __forceinline__ __nv_fp8_e4m3 encode<float, __nv_fp8_e4m3>(float x, float s) { return to_e4m3(x, s); }
+template <> __device__ __forceinline__ __nv_fp8_e4m3 encode<__nv_bfloat16, __nv_fp8_e4m3>(float x, float s) { return to_e4m3(x, s); }
+template <> __device__ __forceinline__ int8_t encode<float, int8_t>(float x, float s) { return to_int8(x, s); }
+template <> __device__ __forceinline__ int8_t encode<__nv_bfloat16, int8_t>(float x, float s) { return to_int8(x, s); }
+template <typename C> constexpr float code_max() { return std::is_same<C, int8_t>::value ? 127.f : 448.f; }
+
+struct WriteArgs {
+  CacheView c;
+  BatchView s;
+  const void* k;
+  const void* v;
+  long long kt, kh, vt, vh;
+  int vec;  // sources and cache rows allow whole-piece accesses
+  FastDiv fd_h, fd_2h;
+  int* err;
+};
+
+// T: elements given, C: elements kept.  Rows are numbered (token, k or v, head).
+template <typename T, typename C, int D>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ WriteArgs a) {
+  constexpr int E = 16 / sizeof(T);  // elements a lane holds of a row
+  constexpr int G = D / E;           // lanes of a row
+  constexpr int RW = 32 / G;         // rows of a warp side by side
+  sm100::grid_dep_launch();
+  sm100::grid_dep_wait();
+  const int lane = threadIdx.x & 31;
+  const long long warp = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const long long rows = (long long)a.s.total_q * 2 * a.c.Hkv;
+  const long long r0 = warp * (RW * kRowsAhead);
+  if (r0 >= rows) return;
+  const int t0 = (int)fdiv((uint32_t)r0, a.fd_2h);
+  const int b0 = a.s.cu_q ? find_seq(a.s.cu_q, a.s.B, t0, lane) : t0;
+
+  float x[kRowsAhead][E];
+  long long dst[kRowsAhead], sdst[kRowsAhead];
+  bool live[kRowsAhead], is_v[kRowsAhead];
+  const int e0 = (lane % G) * E;
+#pragma unroll
+  for (int u = 0; u < kRowsAhead; ++u) {
+    const long long r = r0 + u * RW + lane / G;
+    live[u] = r < rows;
+    const int rr = (int)(live[u] ? r : r0);
+    const int t = (int)fdiv((uint32_t)rr, a.fd_2h);
+    const int kvh = rr - t * 2 * a.c.Hkv;
+    is_v[u] = kvh >= a.c.Hkv;
+    const int h = is_v[u] ? kvh - a.c.Hkv : kvh;
+    const T* src = static_cast<const T*>(is_v[u] ? a.v : a.k) + (is_v[u] ? t * a.vt + h * a.vh : t * a.kt + h * a.kh);
+    if (a.vec) {
+      const uint4 raw = *reinterpret_cast<const uint4*>(src + e0);
+      const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[u][i] = to_f32(e[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[u][i] = to_f32(src[e0 + i]);
+    }
+    // where the row goes: its position in its sequence, through the table
+    int b = b0, pos = -1;
+    if (a.s.cu_q) {
+      while (b + 1 < a.s.B && __ldg(a.s.cu_q + b + 1) <= t) ++b;
+    } else {
+      b = t;
+    }
+    const Seq q = seq_of(a.s, a.c, b, a.err);
+    if (t >= q.q0 && t < q.q0 + q.n) {
+      pos = q.L - q.n + (t - q.q0);
+      if (pos < 0) index_error(a.err);
+    }
+    const int page = pos >= 0 ? page_or_bad(a.s, a.c, b, pos, a.err) : -1;
+    live[u] = live[u] && page >= 0;  // rows behind the last sequence and rows without a place are left out
+    const int off = pos - (int)fdiv((uint32_t)max(pos, 0), a.c.fd_page) * a.c.page_size;
+    dst[u] = is_v[u] ? page * a.c.vp + h * a.c.vh + off * a.c.vt : page * a.c.kp + h * a.c.kh + off * a.c.kt;
+    sdst[u] = is_v[u] ? page * a.c.vsp + h * a.c.vsh + off * a.c.vst : page * a.c.ksp + h * a.c.ksh + off * a.c.kst;
+  }
+#pragma unroll
+  for (int u = 0; u < kRowsAhead; ++u) {
+    float s = 1.f;
+    if (is_code<C>::value) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) m = fmaxf(m, fabsf(x[u][i]));
+#pragma unroll
+      for (int o = 1; o < G; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      s = fmaxf(__fdiv_rn(m, code_max<C>()), kScaleFloor);
+    }
+    if (!live[u]) continue;
+    C* out = static_cast<C*>(is_v[u] ? a.c.v : a.c.k) + dst[u] + e0;
+    alignas(16) C y[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) y[i] = encode<T, C>(x[u][i], s);
+    if (a.vec) {
+      if constexpr (E * sizeof(C) == 16) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(y);
+      else if constexpr (E * sizeof(C) == 8) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
+      else *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<const uint32_t*>(y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) out[i] = y[i];
+    }
+    if (is_code<C>::value && e0 == 0) (is_v[u] ? a.c.vs : a.c.ks)[sdst[u]] = s;
+  }
+}
+
+struct ReadArgs {
+  CacheView c;
+  BatchView s;
+  void* k;
+  void* v;
+  sdpa_strides_t ks, vs;
+  int T, chunks;  // chunks: blocks along the tokens of one (sequence, k or v, head)
+  int vec;
+  FastDiv fd_chunks, fd_h;
+  int* err;
+};
+
+// C: elements kept, T: elements given out.  A block takes a run of tokens of
+// one (sequence, k or v, head): rows that follow each other in a page and in
+// the output.
+template <typename C, typename T, int D>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadArgs a) {
+  constexpr int E = 16 / sizeof(T);
+  constexpr int G = D / E;
+  constexpr int RB = kThreads / G;  // rows of a block side by side
+  sm100::grid_dep_launch();
+  sm100::grid_dep_wait();
+  const uint32_t z = fdiv(blockIdx.x, a.fd_chunks);
+  const int chunk = (int)(blockIdx.x - z * a.chunks);
+  const uint32_t z2 = fdiv(z, a.fd_h);
+  const int h = (int)(z - z2 * a.c.Hkv);
+  const bool is_v = z2 & 1;
+  const int b = (int)(z2 >> 1);
+  const int L = min(seq_len(a.s, a.c, b, a.err), a.T);
+  const int t0 = chunk * (RB * kRowsAhead);
+  if (t0 >= L) return;
+  const int e0 = (threadIdx.x % G) * E;
+  const C* src = static_cast<const C*>(is_v ? a.c.v : a.c.k) + h * (is_v ? a.c.vh : a.c.kh);
+  const float* sc = is_v ? a.c.vs : a.c.ks;
+  if (is_code<C>::value) sc += h * (is_v ? a.c.vsh : a.c.ksh);
+  const long long sp = is_v ? a.c.vp : a.c.kp, stk = is_v ? a.c.vt : a.c.kt;
+  const long long ssp = is_v ? a.c.vsp : a.c.ksp, sst = is_v ? a.c.vst : a.c.kst;
+  const sdpa_strides_t os = is_v ? a.vs : a.ks;
+  T* dst = static_cast<T*>(is_v ? a.v : a.k) + (long long)b * os.b + (long long)h * os.h;
+  int page[kRowsAhead];
+#pragma unroll
+  for (int u = 0; u < kRowsAhead; ++u) {
+    const int t = t0 + u * RB + threadIdx.x / G;
+    page[u] = t < L ? page_of(a.s, a.c, b, t, a.err) : 0;
+  }
+  alignas(16) C raw[kRowsAhead][E];
+  float s[kRowsAhead];
+#pragma unroll
+  for (int u = 0; u < kRowsAhead; ++u) {
+    const int t = t0 + u * RB + threadIdx.x / G;
+    if (t < L) {
+      const int off = t - (int)fdiv((uint32_t)t, a.c.fd_page) * a.c.page_size;
+      const C* row = src + page[u] * sp + off * stk + e0;
+      if (a.vec) {
+        if constexpr (E * sizeof(C) == 16) *reinterpret_cast<uint4*>(raw[u]) = *reinterpret_cast<const uint4*>(row);
+        else if constexpr (E * sizeof(C) == 8) *reinterpret_cast<uint2*>(raw[u]) = *reinterpret_cast<const uint2*>(row);
+        else *reinterpret_cast<uint32_t*>(raw[u]) = *reinterpret_cast<const uint32_t*>(row);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) raw[u][i] = row[i];
+      }
+      s[u] = is_code<C>::value ? sc[page[u] * ssp + off * sst] : 1.f;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kRowsAhead; ++u) {
+    const int t = t0 + u * RB + threadIdx.x / G;
+    if (t < L) {
+      alignas(16) T y[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float f = cache_elem(raw[u][i]);
+        y[i] = from_f32<T>(is_code<C>::value ? f * s[u] : f);
+      }
+      T* o = dst + (long long)t * os.t + e0;
+      if (a.vec) {
+        *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) o[i] = y[i];
+      }
+    }
+  }
+}
+
+// base and strides (in elements of esz bytes) all multiples of n bytes
+bool mult(const void* p, long long a, long long b, long long c, int esz, int n) {
+  return reinterpret_cast<uintptr_t>(p) % n == 0 && (a * esz) % n == 0 && (b * esz) % n == 0 && (c * esz) % n == 0;
+}
+
+template <typename T, typename C, int D>
+cudaError_t write_one(WriteArgs& a, cudaStream_t stream) {
+  constexpr int E = 16 / sizeof(T), RW = 32 / (D / E);
+  const int nb = E * sizeof(C);
+  a.vec = mult(a.k, a.kt, a.kh, 0, sizeof(T), 16) && mult(a.v, a.vt, a.vh, 0, sizeof(T), 16) &&
+          mult(a.c.k, a.c.kp, a.c.kh, a.c.kt, sizeof(C), nb) && mult(a.c.v, a.c.vp, a.c.vh, a.c.vt, sizeof(C), nb);
+  const long long rows = (long long)a.s.total_q * 2 * a.c.Hkv;
+  const long long per = (long long)(kThreads / 32) * RW * kRowsAhead;
+  return launch_serialized(cache_write_kernel<T, C, D>, dim3((unsigned)((rows + per - 1) / per)), dim3(kThreads), 0,
+                           stream, a);
+}
+template <typename T, typename C>
+cudaError_t write_d(WriteArgs& a, cudaStream_t stream) {
+  switch (a.c.d) {
+    case 16: return write_one<T, C, 16>(a, stream);
+    case 64: return write_one<T, C, 64>(a, stream);
+    case 128: return write_one<T, C, 128>(a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename C, typename T, int D>
+cudaError_t read_one(ReadArgs& a, cudaStream_t stream) {
+  constexpr int E = 16 / sizeof(T), RB = kThreads / (D / E);
+  const int nb = E * sizeof(C);
+  a.vec = mult(a.k, a.ks.b, a.ks.h, a.ks.t, sizeof(T), 16) && mult(a.v, a.vs.b, a.vs.h, a.vs.t, sizeof(T), 16) &&
+          mult(a.c.k, a.c.kp, a.c.kh, a.c.kt, sizeof(C), nb) && mult(a.c.v, a.c.vp, a.c.vh, a.c.vt, sizeof(C), nb);
+  a.chunks = (a.T + RB * kRowsAhead - 1) / (RB * kRowsAhead);
+  a.fd_chunks = make_fastdiv((uint32_t)a.chunks);
+  const long long grid = (long long)a.s.B * 2 * a.c.Hkv * a.chunks;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_serialized(cache_read_kernel<C, T, D>, dim3((unsigned)grid), dim3(kThreads), 0, stream, a);
+}
+template <typename C, typename T>
+cudaError_t read_d(ReadArgs& a, cudaStream_t stream) {
+  switch (a.c.d) {
+    case 16: return read_one<C, T, 16>(a, stream);
+    case 64: return read_one<C, T, 64>(a, stream);
+    case 128: return read_one<C, T, 128>(a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheView& c, const BatchView& s, const void* k, long long kt, long long kh,
+                               const void* v, long long vt, long long vh, sdpa_dtype_t dtype, int* err,
+                               cudaStream_t stream) {
+  WriteArgs a;
+  a.c = c; a.s = s; a.k = k; a.v = v; a.kt = kt; a.kh = kh; a.vt = vt; a.vh = vh; a.err = err;
+  a.fd_h = make_fastdiv((uint32_t)c.Hkv);
+  a.fd_2h = make_fastdiv((uint32_t)(2 * c.Hkv));
+  const bool f = dtype == SDPA_F32;
+  switch (c.dtype) {
+    case SDPA_CACHE_F32: return write_d<float, float>(a, stream);
+    case SDPA_CACHE_BF16: return write_d<__nv_bfloat16, __nv_bfloat16>(a, stream);
+    case SDPA_CACHE_E4M3:
+      return f ? write_d<float, __nv_fp8_e4m3>(a, stream) : write_d<__nv_bfloat16, __nv_fp8_e4m3>(a, stream);
+    case SDPA_CACHE_INT8: return f ? write_d<float, int8_t>(a, stream) : write_d<__nv_bfloat16, int8_t>(a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_cache_read(const CacheView& c, const BatchView& s, void* k, const sdpa_strides_t& ks, void* v,
+                              const sdpa_strides_t& vs, sdpa_dtype_t dtype, int T, int* err, cudaStream_t stream) {
+  ReadArgs a;
+  a.c = c; a.s = s; a.k = k; a.v = v; a.ks = ks; a.vs = vs; a.T = T; a.err = err;
+  a.fd_h = make_fastdiv((uint32_t)c.Hkv);
+  const bool f = dtype == SDPA_F32;
+  switch (c.dtype) {
+    case SDPA_CACHE_F32: return read_d<float, float>(a, stream);
+    case SDPA_CACHE_BF16: return read_d<__nv_bfloat16, __nv_bfloat16>(a, stream);
+    case SDPA_CACHE_E4M3:
+      return f ? read_d<__nv_fp8_e4m3, float>(a, stream) : read_d<__nv_fp8_e4m3, __nv_bfloat16>(a, stream);
+    case SDPA_CACHE_INT8: return f ? read_d<int8_t, float>(a, stream) : read_d<int8_t, __nv_bfloat16>(a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace sdpa

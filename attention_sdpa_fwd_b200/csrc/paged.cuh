@@ -1,0 +1,141 @@
+// Shared definitions of the paged key/value cache operators: the kernels'
+// view of a cache and of a ragged batch over it, and the device-side reading
+// of lengths and page numbers, checked before anything is addressed with them.
+//
+// A page number outside the pool, a length the table cannot hold or a query
+// range outside the packed rows comes from device memory the host never sees,
+// so every build checks them: the bad value sets ERR_INDEX in the error word
+// and is replaced by one that stays in bounds (page 0, the nearest length).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "sm100.cuh"
+
+namespace sdpa {
+
+constexpr float kScaleFloor = 9.313225746154785e-10f;  // 2^-30: no row's scale is smaller
+
+struct CacheView {
+  void* k;
+  void* v;
+  float* ks;  // scales of 8-bit codes, else NULL
+  float* vs;
+  long long kp, kh, kt, vp, vh, vt;          // element strides: page, head, token
+  long long ksp, ksh, kst, vsp, vsh, vst;    // of the scales
+  int dtype, num_pages, page_size, Hkv, d;
+  FastDiv fd_page;
+};
+
+struct BatchView {
+  const int* table;
+  long long table_stride;
+  const int* kv_lens;
+  const int* cu_q;  // NULL: one query row per sequence
+  int max_pages, B, total_q, max_q;
+};
+
+struct PagedParams {
+  CacheView c;
+  BatchView s;
+  const void* q;
+  void* out;
+  float* lse;           // optional [total_q, Hq]
+  const float* slopes;  // optional [Hq]
+  long long qt, qh, ot, oh;  // element strides: token, head
+  int Hq, group;
+  float scale, softcap;  // softcap 0: none
+  int window;            // 0: none
+  int* err;
+};
+
+// What the kernels know of one sequence: its packed rows [q0, q0 + n) and its
+// L tokens in the cache; query row i stands at position L - n + i.
+struct Seq {
+  int q0, n, L;
+};
+
+__device__ __forceinline__ void index_error(int* err) {
+  if (err != nullptr) atomicOr(err, ERR_INDEX);
+}
+
+__device__ __forceinline__ int seq_len(const BatchView& s, const CacheView& c, int b, int* err) {
+  const int L = __ldg(s.kv_lens + b);
+  const long long cap = (long long)s.max_pages * c.page_size;
+  if (L < 0 || L > cap) {
+    index_error(err);
+    return L < 0 ? 0 : (int)cap;
+  }
+  return L;
+}
+
+__device__ __forceinline__ Seq seq_of(const BatchView& s, const CacheView& c, int b, int* err) {
+  Seq r;
+  if (s.cu_q == nullptr) {
+    r.q0 = b;
+    r.n = 1;
+  } else {
+    const int a = __ldg(s.cu_q + b), e = __ldg(s.cu_q + b + 1);
+    const bool ok = a >= 0 && e >= a && e <= s.total_q && e - a <= s.max_q;
+    r.q0 = ok ? a : 0;
+    r.n = ok ? e - a : 0;
+    if (!ok) index_error(err);
+  }
+  r.L = seq_len(s, c, b, err);
+  return r;
+}
+
+// Page of token t of sequence b; a bad entry reads as -1.
+__device__ __forceinline__ int page_or_bad(const BatchView& s, const CacheView& c, int b, int t, int* err) {
+  const int p = __ldg(s.table + (long long)b * s.table_stride + fdiv((uint32_t)t, c.fd_page));
+  if ((unsigned)p >= (unsigned)c.num_pages) {
+    index_error(err);
+    return -1;
+  }
+  return p;
+}
+__device__ __forceinline__ int page_of(const BatchView& s, const CacheView& c, int b, int t, int* err) {
+  return max(0, page_or_bad(s, c, b, t, err));
+}
+
+// Keys [lo, hi) a query at position pos sees.
+__device__ __forceinline__ void seen(const PagedParams& p, int pos, int& lo, int& hi) {
+  hi = pos + 1;  // <= L
+  lo = p.window > 0 ? max(0, hi - p.window) : 0;
+}
+
+// Code pairs to f16 pairs (exact): two e4m3 in the low 16 bits; two signed
+// bytes u0, u1 as f16 1024 + (u ^ 128) minus 1152.
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+// bytes at selectors 0..3 of x ^ 0x80808080 already applied by the caller
+__device__ __forceinline__ uint32_t biased_bytes_to_half2(uint32_t x, uint32_t sel) {
+  const uint32_t r = __byte_perm(x, 0x64646464u, sel);
+  __half2 h;
+  memcpy(&h, &r, 4);
+  h = __hsub2(h, __half2{__half_raw{0x6480}, __half_raw{0x6480}});  // 1152
+  uint32_t o;
+  memcpy(&o, &h, 4);
+  return o;
+}
+
+// One element of a cache row as fp32.
+__device__ __forceinline__ float cache_elem(float x) { return x; }
+__device__ __forceinline__ float cache_elem(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float cache_elem(__nv_fp8_e4m3 x) { return float(x); }
+__device__ __forceinline__ float cache_elem(int8_t x) { return (float)x; }
+template <typename C> struct is_code { static constexpr bool value = sizeof(C) == 1; };
+
+cudaError_t launch_cache_write(const CacheView& c, const BatchView& s, const void* k, long long kt, long long kh,
+                               const void* v, long long vt, long long vh, sdpa_dtype_t dtype, int* err,
+                               cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheView& c, const BatchView& s, void* k, const sdpa_strides_t& ks, void* v,
+                              const sdpa_strides_t& vs, sdpa_dtype_t dtype, int T, int* err, cudaStream_t stream);
+cudaError_t launch_paged_exact(const PagedParams& p, sdpa_dtype_t dtype, cudaStream_t stream);
+int* error_word();  // device error word of the current device, NULL if it cannot be had
+
+}  // namespace sdpa

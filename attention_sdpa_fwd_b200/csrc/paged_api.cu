@@ -1,0 +1,201 @@
+// C ABI of the paged key/value cache operators: argument validation, choice of
+// the kernel family, launch.  Declarations and the meaning of every argument:
+// include/sdpa.h.
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "paged.cuh"
+
+namespace sdpa {
+namespace {
+
+constexpr long long kMaxStride = 1LL << 40;
+
+bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+size_t cache_esz(int dtype) { return dtype == SDPA_CACHE_F32 ? 4 : dtype == SDPA_CACHE_BF16 ? 2 : 1; }
+bool is_codes(int dtype) { return dtype == SDPA_CACHE_E4M3 || dtype == SDPA_CACHE_INT8; }
+bool stride_ok(const sdpa_strides_t& s) {
+  return s.b >= 1 && s.h >= 1 && s.t >= 1 && s.b <= kMaxStride && s.h <= kMaxStride && s.t <= kMaxStride;
+}
+bool stride_ok(const sdpa_rows_t& s) { return s.t >= 1 && s.h >= 1 && s.t <= kMaxStride && s.h <= kMaxStride; }
+
+struct Span {
+  uintptr_t lo, hi;
+};
+Span span_of(const void* p, long long elems, size_t esz) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, p == nullptr || elems <= 0 ? a : a + (size_t)elems * esz};
+}
+bool meet(const Span& a, const Span& b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
+long long last3(const sdpa_strides_t& s, long long nb, long long nh, long long nt, long long d) {
+  return nb <= 0 || nh <= 0 || nt <= 0 ? 0 : (nb - 1) * s.b + (nh - 1) * s.h + (nt - 1) * s.t + d;
+}
+long long last2(const sdpa_rows_t& s, long long nt, long long nh, long long d) {
+  return nt <= 0 || nh <= 0 ? 0 : (nt - 1) * s.t + (nh - 1) * s.h + d;
+}
+
+int check_cache(const sdpa_cache_t* c, CacheView* v) {
+  if (c == nullptr) return SDPA_ERR_INVALID_ARG;
+  if (c->dtype < SDPA_CACHE_F32 || c->dtype > SDPA_CACHE_INT8) return SDPA_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->page_size < 1 || c->Hkv < 1) return SDPA_ERR_INVALID_ARG;
+  if (!(c->d == 16 || c->d == 64 || c->d == 128)) return SDPA_ERR_UNSUPPORTED;
+  if (c->k == nullptr || c->v == nullptr) return SDPA_ERR_INVALID_ARG;
+  if (!stride_ok(c->k_strides) || !stride_ok(c->v_strides)) return SDPA_ERR_INVALID_ARG;
+  if (is_codes(c->dtype)) {
+    if (c->k_scale == nullptr || c->v_scale == nullptr) return SDPA_ERR_INVALID_ARG;
+    if (!stride_ok(c->k_scale_strides) || !stride_ok(c->v_scale_strides)) return SDPA_ERR_INVALID_ARG;
+    if (!aligned_to(c->k_scale, 4) || !aligned_to(c->v_scale, 4)) return SDPA_ERR_MISALIGNED;
+  }
+  const size_t esz = cache_esz(c->dtype);
+  if (!aligned_to(c->k, esz) || !aligned_to(c->v, esz)) return SDPA_ERR_MISALIGNED;
+  memset(v, 0, sizeof(*v));
+  v->k = c->k; v->v = c->v;
+  v->kp = c->k_strides.b; v->kh = c->k_strides.h; v->kt = c->k_strides.t;
+  v->vp = c->v_strides.b; v->vh = c->v_strides.h; v->vt = c->v_strides.t;
+  if (is_codes(c->dtype)) {
+    v->ks = c->k_scale; v->vs = c->v_scale;
+    v->ksp = c->k_scale_strides.b; v->ksh = c->k_scale_strides.h; v->kst = c->k_scale_strides.t;
+    v->vsp = c->v_scale_strides.b; v->vsh = c->v_scale_strides.h; v->vst = c->v_scale_strides.t;
+  }
+  v->dtype = c->dtype; v->num_pages = c->num_pages; v->page_size = c->page_size; v->Hkv = c->Hkv; v->d = c->d;
+  v->fd_page = make_fastdiv((uint32_t)c->page_size);
+  return SDPA_OK;
+}
+
+int check_batch(const sdpa_batch_t* s, const CacheView& c, bool rows, BatchView* v) {
+  if (s == nullptr) return SDPA_ERR_INVALID_ARG;
+  if (s->B < 0 || s->max_pages < 0 || s->table_stride < s->max_pages) return SDPA_ERR_INVALID_ARG;
+  if ((long long)s->max_pages * c.page_size > 0x7fffffffLL - 4096) return SDPA_ERR_UNSUPPORTED;
+  if (s->B > 0 && s->kv_lens == nullptr) return SDPA_ERR_INVALID_ARG;
+  if (s->B > 0 && s->max_pages > 0 && s->page_table == nullptr) return SDPA_ERR_INVALID_ARG;
+  if (!aligned_to(s->page_table, 4) || !aligned_to(s->kv_lens, 4) || !aligned_to(s->cu_q, 4)) return SDPA_ERR_MISALIGNED;
+  memset(v, 0, sizeof(*v));
+  v->table = s->page_table; v->table_stride = s->table_stride; v->max_pages = s->max_pages;
+  v->kv_lens = s->kv_lens; v->B = s->B;
+  if (rows) {
+    if (s->total_q < 0 || s->max_q < 0) return SDPA_ERR_INVALID_ARG;
+    if (s->cu_q == nullptr && s->total_q != s->B) return SDPA_ERR_INVALID_ARG;
+    if (s->B == 0 && s->total_q > 0) return SDPA_ERR_INVALID_ARG;
+    v->cu_q = s->cu_q; v->total_q = s->total_q;
+    v->max_q = s->cu_q == nullptr ? 1 : s->max_q < s->total_q ? s->max_q : s->total_q;
+  }
+  return SDPA_OK;
+}
+
+int build_paged(const void* q, const sdpa_rows_t* qs, const sdpa_cache_t* cache, const sdpa_batch_t* batch, void* out,
+                const sdpa_rows_t* os, sdpa_dtype_t dtype, int Hq, float scale, int window, float softcap,
+                const float* slopes, float* lse, PagedParams* p) {
+  memset(p, 0, sizeof(*p));
+  if (dtype != SDPA_F32 && dtype != SDPA_BF16) return SDPA_ERR_INVALID_ARG;
+  int rc = check_cache(cache, &p->c);
+  if (rc == SDPA_OK) rc = check_batch(batch, p->c, true, &p->s);
+  if (rc != SDPA_OK) return rc;
+  if (Hq < 1 || Hq % p->c.Hkv != 0) return SDPA_ERR_INVALID_ARG;
+  if (Hq > 65535) return SDPA_ERR_UNSUPPORTED;
+  if (!is_codes(p->c.dtype) && (p->c.dtype == SDPA_CACHE_F32) != (dtype == SDPA_F32)) return SDPA_ERR_UNSUPPORTED;
+  if (!isfinite(scale) || !isfinite(softcap) || softcap < 0.f || window < 0) return SDPA_ERR_INVALID_ARG;
+  const int d = p->c.d;
+  const sdpa_rows_t dense = {(int64_t)Hq * d, d};
+  const sdpa_rows_t a = qs ? *qs : dense, o = os ? *os : dense;
+  if (!stride_ok(a) || !stride_ok(o)) return SDPA_ERR_INVALID_ARG;
+  p->q = q; p->out = out; p->lse = lse; p->slopes = slopes;
+  p->qt = a.t; p->qh = a.h; p->ot = o.t; p->oh = o.h;
+  p->Hq = Hq; p->group = Hq / p->c.Hkv;
+  p->scale = scale; p->softcap = softcap; p->window = window;
+  const int T = p->s.total_q;
+  if (T == 0) return SDPA_OK;
+  if (q == nullptr || out == nullptr) return SDPA_ERR_INVALID_ARG;
+  const size_t esz = dtype == SDPA_F32 ? 4 : 2, ce = cache_esz(p->c.dtype);
+  if (!aligned_to(q, esz) || !aligned_to(out, esz) || !aligned_to(lse, 4) || !aligned_to(slopes, 4))
+    return SDPA_ERR_MISALIGNED;
+  const Span sq = span_of(q, last2(a, T, Hq, d), esz), so = span_of(out, last2(o, T, Hq, d), esz);
+  const Span sl = span_of(lse, (long long)T * Hq, 4);
+  const Span sk = span_of(cache->k, last3(cache->k_strides, cache->num_pages, cache->Hkv, cache->page_size, d), ce);
+  const Span sv = span_of(cache->v, last3(cache->v_strides, cache->num_pages, cache->Hkv, cache->page_size, d), ce);
+  if (meet(so, sq) || meet(so, sk) || meet(so, sv) || meet(sl, so) || meet(sl, sq) || meet(sl, sk) || meet(sl, sv))
+    return SDPA_ERR_INVALID_ARG;
+  return SDPA_OK;
+}
+
+}  // namespace
+}  // namespace sdpa
+
+using namespace sdpa;
+
+extern "C" int sdpa_cache_write(const sdpa_cache_t* cache, const sdpa_batch_t* batch, const void* k,
+                                const sdpa_rows_t* k_strides, const void* v, const sdpa_rows_t* v_strides,
+                                sdpa_dtype_t dtype, cudaStream_t stream) {
+  CacheView c;
+  BatchView s;
+  if (dtype != SDPA_F32 && dtype != SDPA_BF16) return SDPA_ERR_INVALID_ARG;
+  int rc = check_cache(cache, &c);
+  if (rc == SDPA_OK) rc = check_batch(batch, c, true, &s);
+  if (rc != SDPA_OK) return rc;
+  if (!is_codes(c.dtype) && (c.dtype == SDPA_CACHE_F32) != (dtype == SDPA_F32)) return SDPA_ERR_UNSUPPORTED;
+  const sdpa_rows_t dense = {(int64_t)c.Hkv * c.d, c.d};
+  const sdpa_rows_t ks = k_strides ? *k_strides : dense, vs = v_strides ? *v_strides : dense;
+  if (!stride_ok(ks) || !stride_ok(vs)) return SDPA_ERR_INVALID_ARG;
+  if (s.total_q == 0) return SDPA_OK;
+  if ((long long)s.total_q * 2 * c.Hkv > 0x7fffffffLL) return SDPA_ERR_UNSUPPORTED;
+  if (k == nullptr || v == nullptr) return SDPA_ERR_INVALID_ARG;
+  const size_t esz = dtype == SDPA_F32 ? 4 : 2, ce = cache_esz(c.dtype);
+  if (!aligned_to(k, esz) || !aligned_to(v, esz)) return SDPA_ERR_MISALIGNED;
+  const Span sk = span_of(k, last2(ks, s.total_q, c.Hkv, c.d), esz), sv = span_of(v, last2(vs, s.total_q, c.Hkv, c.d), esz);
+  const Span ck = span_of(c.k, last3(cache->k_strides, c.num_pages, c.Hkv, c.page_size, c.d), ce);
+  const Span cv = span_of(c.v, last3(cache->v_strides, c.num_pages, c.Hkv, c.page_size, c.d), ce);
+  if (meet(sk, ck) || meet(sk, cv) || meet(sv, ck) || meet(sv, cv)) return SDPA_ERR_INVALID_ARG;
+  int* err = error_word();
+  if (err == nullptr) return SDPA_ERR_CUDA;
+  return launch_cache_write(c, s, k, ks.t, ks.h, v, vs.t, vs.h, dtype, err, stream) == cudaSuccess ? SDPA_OK
+                                                                                                  : SDPA_ERR_CUDA;
+}
+
+extern "C" int sdpa_cache_read(const sdpa_cache_t* cache, const sdpa_batch_t* batch, void* k_out,
+                               const sdpa_strides_t* k_strides, void* v_out, const sdpa_strides_t* v_strides,
+                               sdpa_dtype_t dtype, int T, cudaStream_t stream) {
+  CacheView c;
+  BatchView s;
+  if (dtype != SDPA_F32 && dtype != SDPA_BF16) return SDPA_ERR_INVALID_ARG;
+  if (T < 0) return SDPA_ERR_INVALID_ARG;
+  int rc = check_cache(cache, &c);
+  if (rc == SDPA_OK) rc = check_batch(batch, c, false, &s);
+  if (rc != SDPA_OK) return rc;
+  if (!is_codes(c.dtype) && (c.dtype == SDPA_CACHE_F32) != (dtype == SDPA_F32)) return SDPA_ERR_UNSUPPORTED;
+  const sdpa_strides_t dense = {(int64_t)c.Hkv * T * c.d, (int64_t)T * c.d, c.d};
+  const sdpa_strides_t ks = k_strides ? *k_strides : dense, vs = v_strides ? *v_strides : dense;
+  if (s.B == 0 || T == 0) return SDPA_OK;
+  if (!stride_ok(ks) || !stride_ok(vs)) return SDPA_ERR_INVALID_ARG;
+  if ((long long)s.B * 2 * c.Hkv * ((T + 31) / 32) > 0x7fffffffLL) return SDPA_ERR_UNSUPPORTED;
+  if (k_out == nullptr || v_out == nullptr) return SDPA_ERR_INVALID_ARG;
+  const size_t esz = dtype == SDPA_F32 ? 4 : 2, ce = cache_esz(c.dtype);
+  if (!aligned_to(k_out, esz) || !aligned_to(v_out, esz)) return SDPA_ERR_MISALIGNED;
+  const Span ok = span_of(k_out, last3(ks, s.B, c.Hkv, T, c.d), esz), ov = span_of(v_out, last3(vs, s.B, c.Hkv, T, c.d), esz);
+  const Span ck = span_of(c.k, last3(cache->k_strides, c.num_pages, c.Hkv, c.page_size, c.d), ce);
+  const Span cv = span_of(c.v, last3(cache->v_strides, c.num_pages, c.Hkv, c.page_size, c.d), ce);
+  if (meet(ok, ck) || meet(ok, cv) || meet(ov, ck) || meet(ov, cv)) return SDPA_ERR_INVALID_ARG;
+  int* err = error_word();
+  if (err == nullptr) return SDPA_ERR_CUDA;
+  return launch_cache_read(c, s, k_out, ks, v_out, vs, dtype, T, err, stream) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+extern "C" int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const sdpa_cache_t* cache,
+                          const sdpa_batch_t* batch, void* out, const sdpa_rows_t* out_strides, sdpa_dtype_t dtype,
+                          int Hq, float scale, int window, float softcap, const float* slopes, float* lse, int path,
+                          void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
+  if (path < SDPA_PAGED_AUTO || path > SDPA_PAGED_EXACT) return SDPA_ERR_INVALID_ARG;
+  PagedParams p;
+  const int rc = build_paged(q, q_strides, cache, batch, out, out_strides, dtype, Hq, scale, window, softcap, slopes, lse, &p);
+  if (rc != SDPA_OK) return rc;
+  if (p.s.total_q == 0) return SDPA_OK;
+  p.err = error_word();
+  if (p.err == nullptr) return SDPA_ERR_CUDA;
+  (void)workspace; (void)workspace_bytes;
+  return launch_paged_exact(p, dtype, stream) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+extern "C" int64_t sdpa_fwd_paged_workspace(const sdpa_cache_t* cache, const sdpa_batch_t* batch, sdpa_dtype_t dtype, int Hq,
+                                        int path) {
+  (void)cache; (void)batch; (void)dtype; (void)Hq; (void)path;
+  return 0;
+}

@@ -100,8 +100,9 @@ typedef enum {
   SDPA_ERR_TIMEOUT = -5,      /* a device-side bounded wait expired (see
                                  sdpa_last_device_error) */
   SDPA_ERR_CAPACITY = -6,     /* the request exceeds a fixed-size buffer of this entry point */
-  SDPA_ERR_DEVICE_INDEX = -7  /* debug build only: a kernel's device-side index check failed
-                                 (see sdpa_debug_checks) */
+  SDPA_ERR_DEVICE_INDEX = -7  /* a bad page, length or query range of a paged batch, or, in a debug
+                                 build, a kernel's device-side index check failed (see
+                                 sdpa_debug_checks) */
 } sdpa_status;
 
 /* Kernel families.  AUTO picks per shape; the others force one family and
@@ -288,9 +289,129 @@ int sdpa_fwd_split_kv_static(const void* q, const void* k, const void* v, void* 
                              int B, int Hq, int Hkv, int Tq, int Tkv, int d, float scale,
                              int mask_kind, const void* mask_ptr, float* lse, cudaStream_t stream);
 
+/*
+ * ------------------------------------------------------------------ paged key/value cache
+ *
+ * A cache is a pool of `num_pages` pages of `page_size` token rows for each of
+ * Hkv heads, [num_pages, Hkv, page_size, d] or any other order by its strides
+ * (page, head, token; d contiguous).  F32 and BF16 pages hold the rows as
+ * given (in the I/O dtype); E4M3 and INT8 pages hold codes, with one f32 scale
+ * per (page, head, token) row:
+ *     scale = max(f32(amax |x| / Q), 2^-30),  Q = 448 (E4M3) or 127 (INT8)
+ *     code  = round_to_type(f32(x / scale)), ties to even, saturated
+ *     value = code * scale
+ * amax skips NaN elements; a NaN becomes the E4M3 NaN or the INT8 code 0, and
+ * a row with an infinity gets an infinite scale (its finite elements code 0).
+ * Scales a caller writes itself must be positive, finite, at least 2^-30.
+ *
+ * A batch is B sequences: sequence b has kv_lens[b] tokens in the cache,
+ * token t in row t % page_size of page page_table[b * table_stride + t /
+ * page_size] (table entries past its tokens are not read), and n_b new query
+ * rows, packed one sequence after the other: rows cu_q[b] .. cu_q[b+1]-1 of
+ * total_q (cu_q NULL: one row each, total_q == B), at most max_q of them.  The
+ * new rows are the sequence's LAST tokens: row i is at position
+ * kv_lens[b] - n_b + i.  Rows behind cu_q[B] belong to nobody and are left as
+ * they are.  Tables, lengths and cu_q are device memory, read by the kernels
+ * in stream order, so a captured call replays with the lengths of the replay.
+ *
+ * What the host cannot check the kernels do, in every build: a page number
+ * outside the pool, a length below 0 or past max_pages * page_size, a query
+ * range that is decreasing, past total_q or longer than max_q, a write in
+ * front of position 0.  Such a value addresses nothing -- a bad page reads as
+ * page 0, a bad row is not written, a bad query range is empty -- and sets the
+ * device error word (sdpa_last_device_error: SDPA_ERR_DEVICE_INDEX); the
+ * results of that sequence are then unspecified.
+ */
+typedef enum { SDPA_CACHE_F32 = 0, SDPA_CACHE_BF16 = 1, SDPA_CACHE_E4M3 = 2, SDPA_CACHE_INT8 = 3 } sdpa_cache_dtype_t;
+
+typedef struct {
+  void* k;                        /* device, [num_pages, Hkv, page_size, d] by k_strides */
+  void* v;
+  float* k_scale;                 /* device, [num_pages, Hkv, page_size] by k_scale_strides; E4M3 / INT8 only */
+  float* v_scale;
+  int dtype;                      /* sdpa_cache_dtype_t */
+  int num_pages, page_size, Hkv;  /* >= 1 each */
+  int d;                          /* 16, 64 or 128 */
+  sdpa_strides_t k_strides, v_strides, k_scale_strides, v_scale_strides;  /* elements; b is the page axis */
+} sdpa_cache_t;
+
+typedef struct {
+  const int32_t* page_table;  /* device [B, max_pages] */
+  int64_t table_stride;       /* elements between two sequences' rows, >= max_pages */
+  int max_pages;
+  const int32_t* kv_lens;     /* device [B] */
+  const int32_t* cu_q;        /* device [B + 1] or NULL */
+  int B, total_q, max_q;      /* total_q, max_q, cu_q: unused by sdpa_cache_read */
+} sdpa_batch_t;
+
+/* Element strides of the token and head axes of packed rows [tokens, H, d];
+   NULL: dense {H * d, d}. */
+typedef struct {
+  int64_t t;
+  int64_t h;
+} sdpa_rows_t;
+
+/*
+ * sdpa_cache_write -- puts the new rows k, v [total_q, Hkv, d] (dtype F32 or
+ * BF16; F32 / BF16 caches take their own type only) into their pages, quantised
+ * for an E4M3 / INT8 cache.  kv_lens already counts the new tokens.  Two rows
+ * that a table sends to the same place leave either one there, or a mixture.
+ * k and v must not overlap the cache.
+ */
+int sdpa_cache_write(const sdpa_cache_t* cache, const sdpa_batch_t* batch, const void* k, const sdpa_rows_t* k_strides,
+                     const void* v, const sdpa_rows_t* v_strides, sdpa_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * sdpa_cache_read -- the other way: tokens 0 .. min(kv_lens[b], T) - 1 of every
+ * sequence into dense k_out, v_out [B, Hkv, T, d] (any strides; NULL: dense
+ * bhsd, as sdpa_fwd takes them), dequantised and rounded once to dtype.  Rows
+ * past a sequence's tokens are left as they are.
+ */
+int sdpa_cache_read(const sdpa_cache_t* cache, const sdpa_batch_t* batch, void* k_out, const sdpa_strides_t* k_strides,
+                    void* v_out, const sdpa_strides_t* v_strides, sdpa_dtype_t dtype, int T, cudaStream_t stream);
+
+/* Kernel families of sdpa_fwd_paged. */
+typedef enum {
+  SDPA_PAGED_AUTO = 0,
+  SDPA_PAGED_EXACT = 1  /* CUDA cores, fp32 arithmetic; every type, layout and option */
+} sdpa_paged_path_t;
+
+/*
+ * sdpa_fwd_paged -- attention of every sequence's new rows over its cache.  Query
+ * row i of sequence b, at pos = kv_lens[b] - n_b + i, sees the keys j <= pos
+ * (with window w > 0: j > pos - w as well), with scores
+ *     x = scale * q . k_j;   softcap c > 0: x = c * tanh(x / c);
+ *     slopes given: x += slopes[h] * (j - pos)
+ * and out = softmax(x) . v over them; query head h reads kv head h / (Hq/Hkv).
+ * A row that sees no key (pos < 0) is zero, with lse = -inf.
+ *   q, out   : [total_q, Hq, d], any token / head strides, dtype F32 (F32,
+ *              E4M3, INT8 caches) or BF16 (BF16, E4M3, INT8 caches).  out
+ *              must not overlap q or the cache.
+ *   slopes   : device float [Hq] or NULL.
+ *   lse      : NULL or device float [total_q, Hq], the natural-log sum-exp of
+ *              each row's scores; overlaps nothing else.
+ *   path     : sdpa_paged_path_t.
+ *   workspace: device scratch of at least sdpa_fwd_paged_workspace() bytes,
+ *              16-byte aligned, the call's own until its work on `stream` has
+ *              run (SDPA_ERR_CAPACITY when too small).  Nothing is kept in it
+ *              from call to call and it needs no clearing.
+ * Values in rows of the cache that the batch's tokens do not cover may be
+ * anything; those of V rows it does cover must be finite, seen or not.
+ */
+int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const sdpa_cache_t* cache, const sdpa_batch_t* batch,
+               void* out, const sdpa_rows_t* out_strides, sdpa_dtype_t dtype, int Hq, float scale, int window,
+               float softcap, const float* slopes, float* lse, int path, void* workspace, int64_t workspace_bytes,
+               cudaStream_t stream);
+
+/* Bytes of scratch sdpa_fwd_paged needs for calls of these sizes (0: none), or a
+   negative sdpa_status.  Looks at the sizes, strides and alignment only,
+   launches nothing. */
+int64_t sdpa_fwd_paged_workspace(const sdpa_cache_t* cache, const sdpa_batch_t* batch, sdpa_dtype_t dtype, int Hq, int path);
+
 /* Synchronises `stream`, then returns and clears the device error word of the
-   current device: SDPA_OK; SDPA_ERR_DEVICE_INDEX when, in a debug build, a
-   kernel's index check failed since the last call; SDPA_ERR_TIMEOUT when a
+   current device: SDPA_OK; SDPA_ERR_DEVICE_INDEX when a paged operator met a
+   bad page, length or query range, or, in a debug build, a kernel's index
+   check failed since the last call; SDPA_ERR_TIMEOUT when a
    kernel gave up a bounded wait since the last call (output undefined in
    either case); or SDPA_ERR_CUDA when the synchronisation itself failed. */
 int sdpa_last_device_error(cudaStream_t stream);

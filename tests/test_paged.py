@@ -1,0 +1,175 @@
+"""The paged cache operators on the GPU against their definitions in 64 bits."""
+from __future__ import annotations
+
+import itertools
+import math
+
+import pytest
+import torch
+
+import attention_sdpa_fwd_b200 as S
+import paged_ref as R
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, E4M3, INT8 = torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.int8
+
+
+def device_error():
+    torch.cuda.synchronize()
+    return S.sdpa_last_device_error(torch.cuda.current_stream().cuda_stream)
+
+
+def cu(n):
+    return torch.tensor([0] + list(itertools.accumulate(n)), dtype=torch.int32, device="cuda")
+
+
+def bits(t):
+    return t.view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()]).cpu()
+
+
+# ------------------------------------------------------------------ write and read
+WRITES = [  # cache, io, Hkv, d, page, tokens, new rows (None: one each, without cu_q)
+    (BF16, BF16, 8, 128, 16, [20, 1, 300], None),
+    (BF16, BF16, 1, 64, 5, [7, 64, 1], [7, 3, 1]),
+    (F32, F32, 3, 16, 16, [33, 16], [17, 0]),
+    (E4M3, BF16, 8, 128, 32, [500, 31, 1], [100, 0, 1]),
+    (E4M3, F32, 2, 64, 7, [40, 9], [40, 9]),
+    (INT8, BF16, 12, 64, 64, [129, 4], [66, 4]),
+    (INT8, F32, 1, 16, 1, [11], [5]),
+    (E4M3, BF16, 2, 16, 128, [1000], [999]),
+]
+
+
+@pytest.mark.parametrize("layout", ["hnd", "nhd"])
+@pytest.mark.parametrize("cdt,io,Hkv,d,page,kv,n", WRITES)
+def test_write_then_read(cdt, io, Hkv, d, page, kv, n, layout):
+    pool = R.Pool(cdt, Hkv, d, page, kv, seed=3)
+    cache = pool.cache(layout)
+    before = [bits(t).clone() for t in (cache.k, cache.v)]
+    rows = n if n is not None else [1] * len(kv)
+    g = torch.Generator().manual_seed(9)
+    new = [(torch.randn(sum(rows) + 2, Hkv, d, generator=g) * 3).to(io) for _ in range(2)]  # two rows belong to nobody
+    new[0][0] = 0
+    if sum(rows) > 2:
+        new[1][1] *= 1e-12   # below the floor of the scale
+        new[1][2] *= 1e12
+    dev = [x.cuda() for x in new]
+    if n is None:
+        dev = [x[:-2] for x in dev]
+    S.cache_write(cache, dev[0], dev[1], pool.table.cuda(), pool.lens.cuda(), None if n is None else cu(n),
+                  max_q=max(rows))
+    assert device_error() == 0
+    for w, (raw, old) in enumerate(zip((cache.k, cache.v), before)):
+        got = bits(raw)
+        touched = torch.zeros(got.shape[0], page, dtype=torch.bool)
+        at = 0
+        for b, m in enumerate(rows):
+            for i in range(m):
+                j = kv[b] - m + i
+                p, o = pool.table[b, j // page].long(), j % page
+                touched[p, o] = True
+                x = new[w][at + i]
+                if cdt in R.QMAX:
+                    c, s = R.quantise(x, cdt)
+                    assert torch.equal(bits(c.float().to(cdt)), got[p, :, o]) or \
+                        torch.equal(c, raw[p, :, o].cpu().double()), "codes"
+                    sc = (cache.k_scale, cache.v_scale)[w][p, :, o].cpu()
+                    assert torch.equal(sc, s.float()), "scales"
+                else:
+                    assert torch.equal(bits(x.to(cdt)), got[p, :, o])
+            at += m
+        keep = ~touched[:, None, :, None].expand_as(got)
+        assert torch.equal(got[keep], old[keep]), "rows of other tokens changed"
+    # read back: values of the codes, one rounding; rows past the tokens kept
+    out = F32 if cdt in R.QMAX and io == F32 else (cdt if cdt not in R.QMAX else BF16)
+    T = max(kv) + 3
+    if layout == "nhd":
+        ko, vo = (torch.full((len(kv), T, Hkv, d), 7.0, dtype=out, device="cuda").transpose(1, 2) for _ in range(2))
+    else:
+        ko, vo = (torch.full((len(kv), Hkv, T, d), 7.0, dtype=out, device="cuda") for _ in range(2))
+    S.cache_read(cache, pool.table.cuda(), pool.lens.cuda(), ko, vo)
+    assert device_error() == 0
+    for raw, sc, o in ((cache.k, cache.k_scale, ko), (cache.v, cache.v_scale, vo)):
+        full = raw.cpu().float()
+        if sc is not None:
+            full = full * sc.cpu()[..., None]
+        for b, L in enumerate(kv):
+            j = torch.arange(L)
+            want = full[pool.table[b, j // page].long(), :, j % page].transpose(0, 1).to(out)
+            got = o[b, :, :L].cpu()
+            assert torch.equal(bits(want.contiguous()), bits(got.contiguous())) or \
+                torch.equal(want.nan_to_num(), got.nan_to_num())
+            assert (o[b, :, L:] == 7).all()
+
+
+def test_write_odd_strides_and_infinities():
+    """Sources and pools that no 16-byte access fits; NaN and infinities in a row."""
+    pool = R.Pool(INT8, 2, 64, 16, [30], seed=1)
+    base = torch.zeros(4, 2 * 2 * 64 + 1, dtype=BF16, device="cuda")
+    k = torch.as_strided(base, (4, 2, 64), (base.stride(0), 64, 1), 1)
+    k.copy_(torch.randn(4, 2, 64))
+    v = torch.randn(4, 2, 64, device="cuda").to(BF16)
+    v[1, 0, 3] = math.inf
+    v[2, 1, 5] = math.nan
+    cache = pool.cache()
+    wide = torch.zeros(cache.k.shape[0], 2, 16, 65, dtype=INT8, device="cuda")
+    cache = S.KVCache(wide[..., :64], cache.v, cache.k_scale, cache.v_scale)
+    S.cache_write(cache, k, v, pool.table.cuda(), pool.lens.cuda(), cu([4]), max_q=4)
+    assert device_error() == 0
+    for i in range(4):
+        p, o = pool.table[0, (26 + i) // 16].long(), (26 + i) % 16
+        c, s = R.quantise(k[i].cpu(), INT8)
+        assert torch.equal(cache.k[p, :, o].cpu().double(), c)
+        assert (wide[p, :, o, 64] == 0).all()
+    p, o = pool.table[0, 27 // 16].long(), 27 % 16
+    assert torch.isinf(cache.v_scale[p, 0, o]) and (cache.v[p, 0, o] == 0).all()
+    p, o = pool.table[0, 28 // 16].long(), 28 % 16
+    x = v[2, 1].cpu().clone()
+    x[5] = 0
+    c, s = R.quantise(x, INT8)
+    assert torch.equal(cache.v[p, 1, o].cpu().double(), c) and cache.v_scale[p, 1, o].item() == s.item()
+
+
+# ------------------------------------------------------------------ attention
+def run_case(path, cdt, io, Hq, Hkv, d, page, kv, n, *, layout="hnd", window=0, softcap=0.0, slopes=False, seed=0,
+             scale=None, qstd=1.0, **kw):
+    pool = R.Pool(cdt, Hkv, d, page, kv, seed=seed)
+    rows = n if n is not None else [1] * len(kv)
+    g = torch.Generator().manual_seed(seed + 100)
+    q = (torch.randn(sum(rows), Hq, d, generator=g) * qstd).to(io)
+    sl = 2.0 ** (-8.0 * torch.arange(1, Hq + 1) / Hq) if slopes else None
+    lse = torch.empty(sum(rows), Hq, device="cuda")
+    out = S.sdpa_paged(q.cuda(), pool.cache(layout), pool.table.cuda(), pool.lens.cuda(), None if n is None else cu(n),
+                       scale, max_q=max(rows + [0]), window=window, softcap=softcap,
+                       slopes=None if sl is None else sl.cuda(), lse=lse, path=path, **kw)
+    assert device_error() == 0
+    u_p = 0.0 if path == "exact" or io == F32 else R.U[torch.float16 if cdt in R.QMAX else BF16]
+    want, wlse, tol, ltol = R.attend(pool, q, rows, scale=scale, window=window, softcap=softcap, slopes=sl, u_p=u_p)
+    what = f"{path} {cdt} {Hq}/{Hkv} d{d} page {page} kv {kv} n {n} w{window} c{softcap} s{slopes}"
+    R.check(out, want, tol, io, what)
+    R.check_lse(lse, wlse, ltol, what)
+    return out
+
+
+TYPES = [(F32, F32), (BF16, BF16), (E4M3, BF16), (INT8, BF16), (E4M3, F32), (INT8, F32)]
+
+
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("cdt,io", TYPES)
+def test_exact_every_type(cdt, io, d):
+    run_case("exact", cdt, io, 6, 2, d, 16, [1, 17, 200, 33], [1, 5, 2, 33], seed=d)
+    run_case("exact", cdt, io, 3, 3, d, 7, [40, 1, 130], None, seed=d + 1, layout="nhd")
+
+
+@pytest.mark.parametrize("kw", [dict(window=1), dict(window=20), dict(window=1000), dict(softcap=5.0),
+                                dict(slopes=True), dict(window=30, softcap=20.0, slopes=True),
+                                dict(scale=0.0), dict(scale=-0.3), dict(qstd=30.0)])
+@pytest.mark.parametrize("cdt", [BF16, E4M3])
+def test_exact_options(cdt, kw):
+    run_case("exact", cdt, BF16, 4, 2, 64, 16, [100, 31, 64], [10, 31, 1], **kw)
+
+
+def test_exact_more_rows_than_tokens():
+    """New rows in front of the sequence's first token see nothing: zero, -inf."""
+    run_case("exact", BF16, BF16, 4, 2, 64, 16, [3, 0, 20], [5, 2, 4])
