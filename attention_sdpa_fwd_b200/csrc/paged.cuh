@@ -48,6 +48,7 @@ struct PagedParams {
   int Hq, group;
   float scale, softcap;  // softcap 0: none
   int window;            // 0: none
+  int skip_rows;         // the exact kernel leaves out sequences of 1 .. skip_rows (token, head) rows per kv head
   int* err;
 };
 
@@ -136,6 +137,11 @@ cudaError_t launch_cache_write(const CacheView& c, const BatchView& s, const voi
 cudaError_t launch_cache_read(const CacheView& c, const BatchView& s, void* k, const sdpa_strides_t& ks, void* v,
                               const sdpa_strides_t& vs, sdpa_dtype_t dtype, int T, int* err, cudaStream_t stream);
 cudaError_t launch_paged_exact(const PagedParams& p, sdpa_dtype_t dtype, cudaStream_t stream);
+// Sequences of up to this many (token, head) rows per kv head are the decode kernel's.
+constexpr int kDecodeRows = 32;
+int paged_decode_check(const PagedParams& p, sdpa_dtype_t dtype);  // SDPA_OK or why it cannot take the layout
+size_t paged_decode_workspace(const PagedParams& p);
+cudaError_t launch_paged_decode(const PagedParams& p, void* ws, cudaStream_t stream);
 int* error_word();  // device error word of the current device, NULL if it cannot be had
 
 }  // namespace sdpa

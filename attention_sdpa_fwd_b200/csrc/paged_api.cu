@@ -118,6 +118,34 @@ int build_paged(const void* q, const sdpa_rows_t* qs, const sdpa_cache_t* cache,
   return SDPA_OK;
 }
 
+// Which kernels a call takes.  A sequence's rows per kv head decide: the
+// decode kernel has those of up to kDecodeRows; the host only knows the bound
+// max_q, so a batch that may hold both kinds launches both kernels, and each
+// leaves out the other's sequences.
+struct Plan {
+  int status;
+  bool decode, exact;
+  int64_t ws_bytes;
+};
+
+Plan make_plan(const PagedParams& p, sdpa_dtype_t dtype, int path) {
+  Plan r = {SDPA_OK, false, false, 0};
+  const int dec = paged_decode_check(p, dtype);
+  const bool all_few = (long long)p.s.max_q * p.group <= kDecodeRows;
+  switch (path) {
+    case SDPA_PAGED_EXACT: r.exact = true; break;
+    case SDPA_PAGED_DECODE:
+      r.status = dec != SDPA_OK ? dec : all_few ? SDPA_OK : SDPA_ERR_UNSUPPORTED;
+      r.decode = true;
+      break;
+    default:
+      r.decode = dec == SDPA_OK;
+      r.exact = !r.decode || !all_few;
+  }
+  if (r.decode && r.status == SDPA_OK) r.ws_bytes = (int64_t)paged_decode_workspace(p);
+  return r;
+}
+
 }  // namespace
 }  // namespace sdpa
 
@@ -183,19 +211,37 @@ extern "C" int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const
                           const sdpa_batch_t* batch, void* out, const sdpa_rows_t* out_strides, sdpa_dtype_t dtype,
                           int Hq, float scale, int window, float softcap, const float* slopes, float* lse, int path,
                           void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
-  if (path < SDPA_PAGED_AUTO || path > SDPA_PAGED_EXACT) return SDPA_ERR_INVALID_ARG;
+  if (path < SDPA_PAGED_AUTO || path > SDPA_PAGED_DECODE) return SDPA_ERR_INVALID_ARG;
   PagedParams p;
   const int rc = build_paged(q, q_strides, cache, batch, out, out_strides, dtype, Hq, scale, window, softcap, slopes, lse, &p);
   if (rc != SDPA_OK) return rc;
   if (p.s.total_q == 0) return SDPA_OK;
   p.err = error_word();
   if (p.err == nullptr) return SDPA_ERR_CUDA;
-  (void)workspace; (void)workspace_bytes;
-  return launch_paged_exact(p, dtype, stream) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+  const Plan plan = make_plan(p, dtype, path);
+  if (plan.status != SDPA_OK) return plan.status;
+  if (plan.ws_bytes > 0) {
+    if (workspace == nullptr) return SDPA_ERR_INVALID_ARG;
+    if (workspace_bytes < plan.ws_bytes) return SDPA_ERR_CAPACITY;
+    if (!aligned_to(workspace, 16)) return SDPA_ERR_MISALIGNED;
+  }
+  if (plan.decode && launch_paged_decode(p, workspace, stream) != cudaSuccess) return SDPA_ERR_CUDA;
+  if (plan.exact) {
+    p.skip_rows = plan.decode ? kDecodeRows : 0;
+    if (launch_paged_exact(p, dtype, stream) != cudaSuccess) return SDPA_ERR_CUDA;
+  }
+  return SDPA_OK;
 }
 
-extern "C" int64_t sdpa_fwd_paged_workspace(const sdpa_cache_t* cache, const sdpa_batch_t* batch, sdpa_dtype_t dtype, int Hq,
-                                        int path) {
-  (void)cache; (void)batch; (void)dtype; (void)Hq; (void)path;
-  return 0;
+extern "C" int64_t sdpa_fwd_paged_workspace(const sdpa_cache_t* cache, const sdpa_batch_t* batch, const void* q,
+                                            const sdpa_rows_t* q_strides, const void* out,
+                                            const sdpa_rows_t* out_strides, sdpa_dtype_t dtype, int Hq, int path) {
+  if (path < SDPA_PAGED_AUTO || path > SDPA_PAGED_DECODE) return SDPA_ERR_INVALID_ARG;
+  PagedParams p;
+  const int rc = build_paged(q, q_strides, cache, batch, const_cast<void*>(out), out_strides, dtype, Hq, 1.f, 0, 0.f,
+                             nullptr, nullptr, &p);
+  if (rc != SDPA_OK) return rc;
+  if (p.s.total_q == 0) return 0;
+  const Plan plan = make_plan(p, dtype, path);
+  return plan.status != SDPA_OK ? plan.status : plan.ws_bytes;
 }

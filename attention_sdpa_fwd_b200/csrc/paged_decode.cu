@@ -1,0 +1,820 @@
+// Attention over a paged cache for sequences with few new rows: at most 16 or
+// 32 (token, head) rows share a kv head (one new token, or a few drafted ones).
+//
+// HBM-bound: every key and value of the batch is read once, 4 d operations per
+// (row, key) are far below what the bytes leave room for.  So the work is laid
+// out by bytes, not by sequences:
+//
+//  * Work is counted in tiles of kWarps * KS keys of one (sequence, kv head),
+//    all units in one row; CTA c of G takes tiles [T c / G, T (c+1) / G), T from
+//    a scan of the lengths at its start.  Every CTA streams the same number of
+//    bytes whatever the lengths are.  A unit that ends up in several CTAs
+//    leaves unnormalised parts (O, max, sum) in the workspace, at most two per
+//    CTA, and merge_kernel, launched behind, adds them in a fixed order: no
+//    atomics, no state between calls.
+//  * Each warp runs on its own: it copies KS keys and values at a time with
+//    16-byte cp.async into its own ring of NST stages and never waits for
+//    another warp before the end of a unit.  Keys outside the visible range are
+//    filled with zeros without being read (their pages may be gone).
+//  * S = Q.K^T and O += P.V are mma.sync m16n8k16 tiles: at this arithmetic
+//    intensity the tensor pipe is far from its limit and register fragments
+//    save the trips through tensor memory.  The C fragment of S is the A
+//    fragment of P as it stands.
+//
+// 8-bit codes go to f16 without rounding (every e4m3 and int8 value is one).
+// The order of d inside S's sum and of O's columns is free, so a lane takes the
+// codes of its fragments as 16-byte runs of a row: K[key][c D/4 ..] feeds all
+// k-steps of lane c of a quad, V[key][n D/8 ..] column n of every n8 tile, two
+// keys interleaved by byte permutes.  q is scaled by a power of two per row
+// that puts its largest element in [2^14, 2^15), so f16 keeps it to 2^-39 of
+// that.  K's scale multiplies the score's column; V's goes into the exponent:
+//     t_j = x_j log2e + log2 vs_j,  p_j = 2^(t_j - m),  m = max t
+//     out = sum p_j code_j / sum p_j (1 / vs_j)
+// p_j is kept within 2^15 (f16) by m, which may lag 2^3 behind, and offset by
+// 2^12, so that a weight down to 2^-26 of the largest keeps f16's 11 bits and
+// none is off by more than 2^-37 of it; the sums are fp32.
+#include <math.h>
+#include <string.h>
+
+#include "paged.cuh"
+#include "pdl_launch.cuh"
+#include "softmax_tile.cuh"
+
+namespace sdpa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// log2 units the running max may lag behind the largest score, and the offset
+// of P (f16 P: 2^(12 + 3) is below its largest number)
+template <bool F16> constexpr float kLag = F16 ? 3.f : 8.f;
+template <bool F16> constexpr float kOffset = F16 ? 12.f : 0.f;
+
+// KV types
+enum { KV_BF16 = 0, KV_E4M3 = 1, KV_INT8 = 2 };
+
+struct DecodeArgs {
+  PagedParams p;
+  int limit;   // sequences of up to this many rows are this kernel's
+  int whole;   // one CTA per unit, nothing split
+  float* ws_o;      // [2 * CTAs][rows][D]
+  float2* ws_ml;    // [2 * CTAs][rows]
+  long long* ws_first;  // [units] first tile of a unit in the row of all tiles
+  long long* ws_hdr;  // T, CTAs that have work
+};
+
+template <int KV, int D, int MT>
+struct Cfg {
+  static constexpr int kElem = KV == KV_BF16 ? 2 : 1;
+  static constexpr int KS = KV == KV_BF16 ? (D == 128 ? 16 : 32) : 32;  // keys of a warp's step
+  static constexpr int SB = MT == 1 ? KS : 16;                          // keys of one softmax update
+  static constexpr int kRow = D * kElem;
+  static constexpr int kTile = KS * kRow;                               // K (or V) of a step
+  static constexpr int kScales = KV == KV_BF16 ? 0 : 4 * KS * 4;        // ks, vs, log2 vs, 1 / vs
+  static constexpr int kStage = 2 * kTile + kScales;
+  static constexpr int NST = KV != KV_BF16 && D == 64 ? 5 : 3;
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kPitch = D + 4;
+  static constexpr int kRing = kWarps * NST * kStage;
+  static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
+  static constexpr int kQ = MT > 1 ? MT * (D / 16) * 32 * 16 : 0;       // Q fragments in shared memory
+  static constexpr int kBig = kRing > kMergeBytes ? kRing : kMergeBytes;
+  static constexpr int oQ = kBig;
+  static constexpr int oML = oQ + kQ;                                   // [kWarps][kRows] float2
+  static constexpr int kTotal = oML + kWarps * kRows * 8;
+  static constexpr int kKeys = kWarps * KS;                             // keys of a tile
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+  return r;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// four codes to two f16 pairs
+template <int KV>
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (KV == KV_E4M3) {
+    lo = e4m3x2_to_half2(w & 0xffffu);
+    hi = e4m3x2_to_half2(w >> 16);
+  } else {
+    w ^= 0x80808080u;
+    lo = biased_bytes_to_half2(w, 0x4140);
+    hi = biased_bytes_to_half2(w, 0x4342);
+  }
+}
+
+// Where 16-byte piece i of row `key` of a step's K / V tile is kept: an XOR of
+// the piece within its 128-byte line that spreads the 8 lanes of a phase of
+// the fragment loads over all banks.
+template <int KV, int D>
+__device__ __forceinline__ uint32_t k_off(int key, int piece) {
+  if (KV == KV_BF16) return key * (D * 2) + ((piece ^ (key & 7)) << 4);
+  return D == 128 ? key * 128 + ((piece ^ (key & 1)) << 4) : key * 64 + (piece << 4);
+}
+template <int KV, int D>
+__device__ __forceinline__ uint32_t v_off(int key, int piece) {
+  if (KV == KV_BF16) return key * (D * 2) + ((piece ^ (key & 7)) << 4);
+  const int lin = D == 128 ? piece : (key & 1) * 4 + piece;
+  return (D == 128 ? key : key >> 1) * 128 + ((lin ^ (((key >> 1) & 3) << 1)) << 4);
+}
+
+struct Unit {
+  Seq s;
+  int rows;      // n * group
+  int lo16, hi;  // first key (rounded down to 16) and end of what any row sees
+  int lo;
+  int nt;        // tiles
+};
+
+template <int TK>
+__device__ __forceinline__ Unit unit_of(const DecodeArgs& a, int b) {
+  Unit u;
+  u.s = seq_of(a.p.s, a.p.c, b, a.p.err);
+  u.rows = u.s.n * a.p.group;
+  u.hi = u.s.L;
+  u.lo = a.p.window > 0 ? max(0, u.s.L - u.s.n + 1 - a.p.window) : 0;
+  u.lo16 = u.lo & ~15;
+  u.nt = u.rows > 0 && u.rows <= a.limit && u.hi > u.lo ? (u.hi - u.lo16 + TK - 1) / TK : 0;
+  return u;
+}
+
+// CTA that owns tile f of T split over G
+__device__ __forceinline__ int owner(long long f, long long T, int G) { return (int)(((f + 1) * G - 1) / T); }
+
+template <int KV, int D, int MT, bool MOD>
+__global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_constant__ DecodeArgs a) {
+  using C = Cfg<KV, D, MT>;
+  constexpr bool F16 = KV != KV_BF16;
+  constexpr int KS = C::KS, SB = C::SB, NST = C::NST;
+  constexpr float kShift = kOffset<F16>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_b;
+  __shared__ long long s_scan[kWarps], s_F;
+  const PagedParams& p = a.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int quad = lane >> 2, c = lane & 3;
+  grid_dep_wait();
+  grid_dep_launch();  // the merge may start: it reads nothing of this call's inputs that still changes
+
+  const int G = gridDim.x;
+  int b;
+  long long F, cur, end, T = 0;
+  int work_ctas = G;
+  if (a.whole) {
+    b = blockIdx.x / p.c.Hkv;
+    F = 0;
+    const int nt = unit_of<C::kKeys>(a, b).nt;
+    cur = (long long)(blockIdx.x - b * p.c.Hkv) * nt;
+    end = cur + nt;
+  } else {
+    // tiles of all sequences: each thread a run of sequences, then a scan
+    const int per = (p.s.B + kThreads - 1) / kThreads;
+    long long mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const int bb = tid * per + i;
+      if (bb < p.s.B) mine += unit_of<C::kKeys>(a, bb).nt;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    if (tid == 0) { s_b = p.s.B; s_F = 0; }
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) incl += s_scan[w];
+      total += s_scan[w];
+    }
+    T = total * p.c.Hkv;
+    // at least two tiles to a CTA
+    work_ctas = (int)min((long long)G, max(1LL, T / 2));
+    cur = blockIdx.x < work_ctas ? T * blockIdx.x / work_ctas : T;
+    end = blockIdx.x < work_ctas ? T * (blockIdx.x + 1) / work_ctas : T;
+    long long at = (incl - mine) * p.c.Hkv;
+    if (cur < end && cur >= at && cur < at + mine * p.c.Hkv) {
+      int bb = tid * per;
+      for (;; ++bb) {
+        const long long w = (long long)unit_of<C::kKeys>(a, bb).nt * p.c.Hkv;
+        if (cur < at + w) break;
+        at += w;
+      }
+      s_b = bb;
+      s_F = at;
+    }
+    __syncthreads();
+    b = s_b;
+    F = s_F;
+    if (blockIdx.x == 0 && tid == 0) {
+      a.ws_hdr[0] = T;
+      a.ws_hdr[1] = work_ctas;
+    }
+  }
+  const long long begin = cur;
+
+  const uint32_t ring = smem_u32(smem) + warp * (NST * C::kStage);
+  float* mrg = reinterpret_cast<float*>(smem);
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::oML);
+
+  while (cur < end && b < p.s.B) {
+    const Unit u = unit_of<C::kKeys>(a, b);
+    if (u.nt == 0) { ++b; continue; }
+    const int hk = (int)((cur - F) / u.nt);
+    const int tile0 = (int)((cur - F) - (long long)hk * u.nt);
+    const int ntile = (int)min((long long)(u.nt - tile0), end - cur);
+    const int base = u.lo16 + tile0 * C::kKeys + warp * KS;  // this warp's first key
+    const int khi = u.hi, klo = u.lo;
+
+    // ---- the ring: one step is KS keys and values of this warp
+    const uint8_t* kp = static_cast<const uint8_t*>(p.c.k) + (long long)hk * p.c.kh * C::kElem;
+    const uint8_t* vp = static_cast<const uint8_t*>(p.c.v) + (long long)hk * p.c.vh * C::kElem;
+    int pg[KS / 16];
+    auto lookup = [&](int step) {
+      const int t0 = base + step * C::kKeys;
+#pragma unroll
+      for (int g = 0; g < KS / 16; ++g) {
+        const int t = t0 + 16 * g;
+        pg[g] = step < ntile && t < khi && t + 16 > klo ? page_of(p.s, p.c, b, t, p.err) : 0;
+      }
+    };
+    auto issue = [&](int step) {
+      if (step < ntile) {
+        constexpr int kPieces = C::kRow / 16;     // of a row
+        constexpr int kPass = 32 / kPieces;       // rows of a pass
+        const uint32_t st = ring + (step % NST) * C::kStage;
+        const int t0 = base + step * C::kKeys;
+        const int piece = lane % kPieces, r0 = lane / kPieces;
+#pragma unroll
+        for (int i = 0; i < KS / kPass; ++i) {
+          const int r = i * kPass + r0;
+          const int g = (i * kPass) / 16;
+          const int t = t0 + r;
+          const bool live = t >= klo && t < khi;
+          const int off = live ? t - (int)fdiv((uint32_t)t, p.c.fd_page) * p.c.page_size : 0;
+          const uint8_t* ks = kp + ((long long)pg[g] * p.c.kp + (long long)off * p.c.kt) * C::kElem + piece * 16;
+          const uint8_t* vs = vp + ((long long)pg[g] * p.c.vp + (long long)off * p.c.vt) * C::kElem + piece * 16;
+          cp16(st + k_off<KV, D>(r, piece), ks, live);
+          cp16(st + C::kTile + v_off<KV, D>(r, piece), vs, live);
+        }
+        if constexpr (F16) {
+          const int t = t0 + lane;  // KS == 32
+          const bool live = t >= klo && t < khi;
+          const int off = live ? t - (int)fdiv((uint32_t)t, p.c.fd_page) * p.c.page_size : 0;
+          const long long pl = lane < 16 ? pg[0] : pg[KS / 16 - 1];
+          const uint32_t sc = st + 2 * C::kTile + lane * 4;
+          cp4(sc, p.c.ks + pl * p.c.ksp + hk * p.c.ksh + off * p.c.kst, live);
+          cp4(sc + KS * 4, p.c.vs + pl * p.c.vsp + hk * p.c.vsh + off * p.c.vst, live);
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) {
+      lookup(i);
+      issue(i);
+    }
+    lookup(NST - 1);
+
+    // ---- Q as A fragments: row r of the unit is token r / group, head r % group
+    uint32_t qf[MT == 1 ? D / 16 : 1][4];
+    float xscale[MT][2];  // what turns the accumulator of a row into its score
+    int pos[MT][2];
+    float slope[MT][2];
+    const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(p.q);
+    uint32_t* s_q = reinterpret_cast<uint32_t*>(smem + C::oQ);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = m * 16 + e * 8 + quad;
+        const int i = r / p.group, g = r - i * p.group;
+        const bool live = r < u.rows;
+        const int h = hk * p.group + g;
+        const __nv_bfloat16* src = qb + (long long)(u.s.q0 + i) * p.qt + (long long)h * p.qh;
+        pos[m][e] = u.s.L - u.s.n + i;
+        slope[m][e] = MOD && p.slopes && live ? __ldg(p.slopes + h) : 0.f;
+        xscale[m][e] = p.scale;
+        uint32_t w[D / 8];  // this lane's D / 4 elements, in pairs
+        if constexpr (F16) {
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (live) x = *reinterpret_cast<const uint4*>(src + c * (D / 4) + k * 8);
+            w[4 * k] = x.x; w[4 * k + 1] = x.y; w[4 * k + 2] = x.z; w[4 * k + 3] = x.w;
+          }
+          float top = 0.f;
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // 2^k with top 2^k in [2^14, 2^15), k within what a float holds
+          const int ex = top > 0.f && top < INFINITY ? min(126, max(-126, 141 - (int)(__float_as_uint(top) >> 23))) : 0;
+          const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+          xscale[m][e] *= __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) {
+            const __half2 hh = __floats2half2_rn(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
+            memcpy(&w[k], &hh, 4);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k)
+            w[k] = live ? __ldg(reinterpret_cast<const unsigned int*>(src + 16 * (k >> 1) + 8 * (k & 1) + 2 * c)) : 0u;
+        }
+        // pair 2s is a0 / a1 of k-step s, pair 2s + 1 is a2 / a3
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          if constexpr (MT == 1) {
+            qf[s][e] = w[2 * s];
+            qf[s][2 + e] = w[2 * s + 1];
+          } else if (s % kWarps == warp) {  // every warp has the same fragments: each writes a share
+            s_q[((m * (D / 16) + s) * 32 + lane) * 4 + e] = w[2 * s];
+            s_q[((m * (D / 16) + s) * 32 + lane) * 4 + 2 + e] = w[2 * s + 1];
+          }
+        }
+      }
+    }
+    if constexpr (MT > 1) __syncthreads();
+
+    float o[MT][D / 8][4];
+    float mx[MT][2], l[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[m][i][k] = 0.f;
+      mx[m][0] = mx[m][1] = -INFINITY;
+      l[m][0] = l[m][1] = 0.f;
+    }
+    const int pos_first = u.s.L - u.s.n, pos_last = u.s.L - 1;
+    const float icap2 = MOD && p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
+
+    for (int step = 0; step < ntile; ++step) {
+      cp_wait<NST - 2>();
+      __syncwarp();
+      const uint32_t st = ring + (step % NST) * C::kStage;
+      const int t0 = base + step * C::kKeys;
+      float* sc = reinterpret_cast<float*>(smem + (st - smem_u32(smem)) + 2 * C::kTile);
+      if constexpr (F16) {  // log2 vs and 1 / vs of this lane's key; a key not read counts as scale 1
+        const int t = t0 + lane;
+        const float vs = t >= klo && t < khi ? sc[KS + lane] : 1.f;
+        float lg;
+        asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(vs));
+        sc[2 * KS + lane] = lg;
+        sc[3 * KS + lane] = __frcp_rn(vs);
+      }
+      issue(step + NST - 1);
+      lookup(step + NST);
+      if (t0 >= khi || t0 + KS <= klo) continue;  // nothing of it is seen
+      if constexpr (F16) __syncwarp();
+      const bool edge = t0 + KS - 1 > pos_first || t0 < klo || (p.window > 0 && t0 <= pos_last - p.window);
+#pragma unroll
+      for (int sb = 0; sb < KS; sb += SB) {
+        // ---- S = Q.K^T
+        float s[MT][SB / 8][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int n = 0; n < SB / 8; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[m][n][k] = 0.f;
+        if constexpr (F16) {
+          uint32_t w[SB / 8][D / 16];
+#pragma unroll
+          for (int n = 0; n < SB / 8; ++n)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+              const uint4 x = lds16(st + k_off<KV, D>(sb + n * 8 + quad, c * (D / 64) + i));
+              w[n][4 * i] = x.x; w[n][4 * i + 1] = x.y; w[n][4 * i + 2] = x.z; w[n][4 * i + 3] = x.w;
+            }
+#pragma unroll
+          for (int ss = 0; ss < D / 16; ++ss) {
+            uint32_t q4[MT][4];
+            if constexpr (MT > 1) {
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                const uint4 x = lds16(smem_u32(smem) + C::oQ + ((m * (D / 16) + ss) * 32 + lane) * 16);
+                q4[m][0] = x.x; q4[m][1] = x.y; q4[m][2] = x.z; q4[m][3] = x.w;
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < SB / 8; ++n) {
+              uint32_t b0, b1;
+              codes4<KV>(w[n][ss], b0, b1);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                if constexpr (MT > 1) mma<F16>(s[m][n], q4[m], b0, b1);
+                else mma<F16>(s[m][n], qf[ss], b0, b1);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int sp = 0; sp < D / 32; ++sp) {
+            uint32_t q4[MT][2][4];
+            if constexpr (MT > 1) {
+#pragma unroll
+              for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int x2 = 0; x2 < 2; ++x2) {
+                  const uint4 x = lds16(smem_u32(smem) + C::oQ + ((m * (D / 16) + 2 * sp + x2) * 32 + lane) * 16);
+                  q4[m][x2][0] = x.x; q4[m][x2][1] = x.y; q4[m][x2][2] = x.z; q4[m][x2][3] = x.w;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < SB / 8; ++n) {
+              uint32_t r[4];
+              ldsm4(st + k_off<KV, D>(sb + n * 8 + (lane & 7), 4 * sp + (lane >> 3)), r);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                if constexpr (MT > 1) {
+                  mma<F16>(s[m][n], q4[m][0], r[0], r[1]);
+                  mma<F16>(s[m][n], q4[m][1], r[2], r[3]);
+                } else {
+                  mma<F16>(s[m][n], qf[2 * sp], r[0], r[1]);
+                  mma<F16>(s[m][n], qf[2 * sp + 1], r[2], r[3]);
+                }
+              }
+            }
+          }
+        }
+        // ---- scores in log2 units, running max, P
+        uint32_t pf[MT][SB / 16][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          float iv[F16 ? SB / 8 : 1][2];
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int n = 0; n < SB / 8; ++n) {
+            const int kk = sb + n * 8 + 2 * c;
+            float ks2[2] = {1.f, 1.f}, lv2[2] = {0.f, 0.f};
+            if constexpr (F16) {
+              const float2 x = *reinterpret_cast<const float2*>(sc + kk);
+              const float2 y = *reinterpret_cast<const float2*>(sc + 2 * KS + kk);
+              const float2 z = *reinterpret_cast<const float2*>(sc + 3 * KS + kk);
+              ks2[0] = x.x; ks2[1] = x.y; lv2[0] = y.x; lv2[1] = y.y;
+              iv[n][0] = z.x; iv[n][1] = z.y;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = k >> 1, j = t0 + kk + (k & 1);
+              float x;
+              if constexpr (MOD) {
+                float y = s[m][n][k] * xscale[m][e] * ks2[k & 1];
+                if (p.softcap > 0.f)  // c tanh(y / c) = c - 2 c / (1 + e^(2 y / c))
+                  y = fmaf(-2.f * p.softcap, __frcp_rn(1.f + ex2_approx(y * icap2)), p.softcap);
+                y = fmaf(slope[m][e], (float)(j - pos[m][e]), y);
+                x = fmaf(y, kLog2e, lv2[k & 1]);
+              } else if constexpr (F16) {
+                x = fmaf(s[m][n][k] * ks2[k & 1], xscale[m][e] * kLog2e, lv2[k & 1]);
+              } else {
+                x = s[m][n][k] * (xscale[m][e] * kLog2e);
+              }
+              if (edge && (j > pos[m][e] || (p.window > 0 && j <= pos[m][e] - p.window)))
+                x = -INFINITY;
+              s[m][n][k] = x;
+              top[e] = fmaxf(top[e], x);
+            }
+          }
+          bool grow = false;
+          float al[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+            al[e] = 1.f;
+            if (top[e] > mx[m][e] + kLag<F16>) {  // from -inf too; false while both are
+              al[e] = ex2_approx(mx[m][e] - top[e]);
+              mx[m][e] = top[e];
+              grow = true;
+            }
+          }
+          if (__any_sync(0xffffffffu, grow)) {
+            l[m][0] *= al[0];
+            l[m][1] *= al[1];
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              o[m][i][0] *= al[0]; o[m][i][1] *= al[0];
+              o[m][i][2] *= al[1]; o[m][i][3] *= al[1];
+            }
+          }
+          const float ms[2] = {mx[m][0] == -INFINITY ? 0.f : mx[m][0] - kShift,
+                               mx[m][1] == -INFINITY ? 0.f : mx[m][1] - kShift};
+#pragma unroll
+          for (int n = 0; n < SB / 8; ++n) {
+            float w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              w[k] = ex2_approx(s[m][n][k] - ms[k >> 1]);
+              if constexpr (F16) l[m][k >> 1] = fmaf(w[k], iv[n][k & 1], l[m][k >> 1]);
+              else l[m][k >> 1] += w[k];
+            }
+            uint32_t a0, a1;
+            if constexpr (F16) {
+              const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
+              memcpy(&a0, &h0, 4);
+              memcpy(&a1, &h1, 4);
+            } else {
+              a0 = pack_bf16x2(w[0], w[1]);
+              a1 = pack_bf16x2(w[2], w[3]);
+            }
+            pf[m][n >> 1][(n & 1) * 2] = a0;
+            pf[m][n >> 1][(n & 1) * 2 + 1] = a1;
+          }
+        }
+        // ---- O += P.V
+#pragma unroll
+        for (int kg = 0; kg < SB / 16; ++kg) {
+          const int k0 = sb + kg * 16;
+          const uint32_t vt = st + C::kTile;
+          if constexpr (F16) {
+            constexpr int W = D / 32;  // words of a lane's run of a row
+            uint32_t w[4][W];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = k0 + 2 * c + (x & 1) + (x >> 1) * 8;
+              if constexpr (D == 128) {
+                const uint4 y = lds16(vt + v_off<KV, D>(key, quad));
+                w[x][0] = y.x; w[x][1] = y.y; w[x][W - 2] = y.z; w[x][W - 1] = y.w;
+              } else {
+                const uint2 y = lds8(vt + v_off<KV, D>(key, quad >> 1) + (quad & 1) * 8);
+                w[x][0] = y.x; w[x][1] = y.y;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+              uint32_t b0[4], b1[4];
+              codes4<KV>(__byte_perm(w[0][i], w[1][i], 0x5140), b0[0], b0[1]);
+              codes4<KV>(__byte_perm(w[0][i], w[1][i], 0x7362), b0[2], b0[3]);
+              codes4<KV>(__byte_perm(w[2][i], w[3][i], 0x5140), b1[0], b1[1]);
+              codes4<KV>(__byte_perm(w[2][i], w[3][i], 0x7362), b1[2], b1[3]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma<F16>(o[m][4 * i + y], pf[m][kg], b0[y], b1[y]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t r[4];
+              ldsm4t(vt + v_off<KV, D>(k0 + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * i + (lane >> 4)), r);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                mma<F16>(o[m][2 * i], pf[m][kg], r[0], r[1]);
+                mma<F16>(o[m][2 * i + 1], pf[m][kg], r[2], r[3]);
+              }
+            }
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+
+    // ---- the warps' parts into one
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[m][e] += __shfl_xor_sync(0xffffffffu, l[m][e], 1);
+        l[m][e] += __shfl_xor_sync(0xffffffffu, l[m][e], 2);
+        if (c == 0) s_ml[warp * C::kRows + m * 16 + e * 8 + quad] = make_float2(mx[m][e], l[m][e]);
+      }
+    __syncthreads();  // every ring is drained: its space holds the parts now
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = m * 16 + e * 8 + quad;
+        float top = -INFINITY;
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
+        const float f = mx[m][e] == -INFINITY ? 0.f : ex2_approx(mx[m][e] - top);
+        float* dst = mrg + (warp * C::kRows + r) * C::kPitch;
+        if (r < u.rows) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            if constexpr (F16) {
+              dst[(D / 8) * (2 * c) + i] = o[m][i][2 * e] * f;
+              dst[(D / 8) * (2 * c + 1) + i] = o[m][i][2 * e + 1] * f;
+            } else {
+              *reinterpret_cast<float2*>(dst + 8 * i + 2 * c) = make_float2(o[m][i][2 * e] * f, o[m][i][2 * e + 1] * f);
+            }
+          }
+        }
+      }
+    __syncthreads();
+    const bool complete = ntile == u.nt;
+    const long long slot = 2LL * blockIdx.x + (cur == begin ? 0 : 1);
+    if (!a.whole && tile0 == 0 && tid == 0) a.ws_first[(long long)b * p.c.Hkv + hk] = cur;
+    for (int i = tid; i < u.rows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
+      float top = -INFINITY, den = 0.f;
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = s_ml[w * C::kRows + r];
+        if (ml.x != -INFINITY) den = fmaf(ex2_approx(ml.x - top), ml.y, den);
+        const float4 y = *reinterpret_cast<const float4*>(mrg + (w * C::kRows + r) * C::kPitch + x);
+        acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
+      }
+      if (!complete) {
+        *reinterpret_cast<float4*>(a.ws_o + (slot * C::kRows + r) * D + x) = acc;
+        if (x == 0) a.ws_ml[slot * C::kRows + r] = make_float2(top, den);
+      } else {
+        const int tok = r / p.group, h = hk * p.group + r - tok * p.group;
+        const float inv = den > 0.f ? 1.f / den : 0.f;
+        uint2 y;
+        y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+        y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (long long)(u.s.q0 + tok) * p.ot + (long long)h * p.oh;
+        *reinterpret_cast<uint2*>(dst + x) = y;
+        if (x == 0 && p.lse)
+          p.lse[(long long)(u.s.q0 + tok) * p.Hq + h] = den > 0.f ? (top - kShift) * kLn2 + logf(den) : -INFINITY;
+      }
+    }
+    __syncthreads();  // before the next unit's copies land in the ring
+    cur += ntile;
+    if (cur - F == (long long)u.nt * p.c.Hkv) { F = cur; ++b; }
+  }
+
+  // rows that see nothing at all
+  for (int unit = blockIdx.x; unit < p.s.B * p.c.Hkv; unit += G) {
+    const int bb = unit / p.c.Hkv, hk = unit - bb * p.c.Hkv;
+    const Unit u = unit_of<C::kKeys>(a, bb);
+    if (u.nt != 0 || u.rows == 0 || u.rows > a.limit) continue;
+    for (int i = tid; i < u.rows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
+      const int tok = r / p.group, h = hk * p.group + r - tok * p.group;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (long long)(u.s.q0 + tok) * p.ot + (long long)h * p.oh;
+      *reinterpret_cast<uint2*>(dst + x) = make_uint2(0, 0);
+      if (x == 0 && p.lse) p.lse[(long long)(u.s.q0 + tok) * p.Hq + h] = -INFINITY;
+    }
+  }
+}
+
+// Adds the parts of every unit that several CTAs share: O = sum 2^(m_i - M) O_i
+// over sum 2^(m_i - M) l_i, in the order of the tiles.  One block per unit.
+template <int TK, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads) paged_merge_kernel(const __grid_constant__ DecodeArgs a, float shift) {
+  const PagedParams& p = a.p;
+  const int b = blockIdx.x / p.c.Hkv, hk = blockIdx.x - b * p.c.Hkv;
+  grid_dep_wait();
+  grid_dep_launch();
+  const Unit u = unit_of<TK>(a, b);
+  if (u.nt == 0) return;
+  const long long T = a.ws_hdr[0];
+  const int G = (int)a.ws_hdr[1];
+  const long long f = a.ws_first[blockIdx.x];
+  const int c0 = owner(f, T, G), c1 = owner(f + u.nt - 1, T, G);
+  if (c0 == c1) return;
+  for (int i = threadIdx.x; i < u.rows * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
+    auto slot = [&](int cta) { return 2LL * cta + (cta == c0 && f > T * c0 / G ? 1 : 0); };
+    float top = -INFINITY, den = 0.f;
+    for (int q = c0; q <= c1; ++q) top = fmaxf(top, a.ws_ml[slot(q) * ROWS + r].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int q = c0; q <= c1; ++q) {
+      const long long s = slot(q) * ROWS + r;
+      const float2 ml = a.ws_ml[s];
+      const float4 y = *reinterpret_cast<const float4*>(a.ws_o + s * D + x);
+      const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+      den = fmaf(w, ml.y, den);
+      acc.x = fmaf(w, y.x, acc.x); acc.y = fmaf(w, y.y, acc.y);
+      acc.z = fmaf(w, y.z, acc.z); acc.w = fmaf(w, y.w, acc.w);
+    }
+    const int tok = r / p.group, h = hk * p.group + r - tok * p.group;
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    uint2 y;
+    y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+    y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (long long)(u.s.q0 + tok) * p.ot + (long long)h * p.oh;
+    *reinterpret_cast<uint2*>(dst + x) = y;
+    if (x == 0 && p.lse)
+      p.lse[(long long)(u.s.q0 + tok) * p.Hq + h] = den > 0.f ? (top - shift) * kLn2 + logf(den) : -INFINITY;
+  }
+}
+
+template <int KV, int D, int MT>
+cudaError_t decode_one(DecodeArgs& a, bool mod, int ctas, cudaStream_t stream) {
+  using C = Cfg<KV, D, MT>;
+  auto kern = mod ? paged_decode_kernel<KV, D, MT, true> : paged_decode_kernel<KV, D, MT, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
+  if (e != cudaSuccess) return e;
+  e = launch_serialized(kern, dim3((unsigned)ctas), dim3(kThreads), (size_t)C::kTotal, stream, a);
+  if (e != cudaSuccess || a.whole) return e;
+  return launch_serialized(paged_merge_kernel<C::kKeys, D, C::kRows>, dim3((unsigned)(a.p.s.B * a.p.c.Hkv)),
+                           dim3(kThreads), 0, stream, a, kOffset<KV != KV_BF16>);
+}
+template <int KV, int D>
+cudaError_t decode_rows(DecodeArgs& a, bool mod, int ctas, cudaStream_t stream) {
+  return a.limit <= 16 ? decode_one<KV, D, 1>(a, mod, ctas, stream) : decode_one<KV, D, 2>(a, mod, ctas, stream);
+}
+
+// Rows a call's sequences may have here: 16 (one row tile) when no sequence
+// can have more, else 32.
+int row_limit(const PagedParams& p) { return (long long)p.s.max_q * p.group <= 16 ? 16 : kDecodeRows; }
+
+// One CTA per unit and no merge launch where the caches are so short that the
+// longest unit is no more than two tiles of 64 or 128 keys.
+bool whole_units(const PagedParams& p) {
+  const int tile = p.c.dtype == SDPA_CACHE_BF16 && p.c.d == 128 ? 64 : 128;
+  return (long long)p.s.max_pages * p.c.page_size <= 2 * tile;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+int paged_decode_check(const PagedParams& p, sdpa_dtype_t dtype) {
+  const CacheView& c = p.c;
+  if (dtype != SDPA_BF16 || c.dtype == SDPA_CACHE_F32 || c.d == 16) return SDPA_ERR_UNSUPPORTED;
+  if (c.page_size % 16 != 0 || p.group > kDecodeRows) return SDPA_ERR_UNSUPPORTED;
+  if ((long long)p.s.B * c.Hkv > 0x7fffffffLL) return SDPA_ERR_UNSUPPORTED;
+  const long long es = c.dtype == SDPA_CACHE_BF16 ? 2 : 1;
+  const long long bytes[] = {c.kp * es, c.kh * es, c.kt * es, c.vp * es, c.vh * es, c.vt * es, p.qt * 2, p.qh * 2};
+  for (long long x : bytes)
+    if (x % 16 != 0) return SDPA_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) | reinterpret_cast<uintptr_t>(p.q)) % 16 != 0 ||
+      reinterpret_cast<uintptr_t>(p.out) % 8 != 0 || p.ot % 4 != 0 || p.oh % 4 != 0)
+    return SDPA_ERR_MISALIGNED;
+  return SDPA_OK;
+}
+
+size_t paged_decode_workspace(const PagedParams& p) {
+  if (whole_units(p) || p.s.total_q == 0) return 0;
+  const size_t slots = 2 * 2 * (size_t)num_sms(), rows = row_limit(p);
+  return up256(slots * rows * p.c.d * 4) + up256(slots * rows * 8) + up256((size_t)p.s.B * p.c.Hkv * 8) + 256;
+}
+
+cudaError_t launch_paged_decode(const PagedParams& p, void* ws, cudaStream_t stream) {
+  DecodeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.p = p;
+  a.limit = row_limit(p);
+  a.whole = whole_units(p);
+  const int ctas = a.whole ? p.s.B * p.c.Hkv : 2 * num_sms();
+  if (!a.whole) {
+    const size_t slots = 2 * (size_t)ctas, rows = a.limit;
+    char* w = static_cast<char*>(ws);
+    a.ws_o = reinterpret_cast<float*>(w);
+    w += up256(slots * rows * p.c.d * 4);
+    a.ws_ml = reinterpret_cast<float2*>(w);
+    w += up256(slots * rows * 8);
+    a.ws_first = reinterpret_cast<long long*>(w);
+    w += up256((size_t)p.s.B * p.c.Hkv * 8);
+    a.ws_hdr = reinterpret_cast<long long*>(w);
+  }
+  const bool mod = p.softcap > 0.f || p.slopes != nullptr;
+  const bool wide = p.c.d == 128;
+  switch (p.c.dtype) {
+    case SDPA_CACHE_BF16: return wide ? decode_rows<KV_BF16, 128>(a, mod, ctas, stream) : decode_rows<KV_BF16, 64>(a, mod, ctas, stream);
+    case SDPA_CACHE_E4M3: return wide ? decode_rows<KV_E4M3, 128>(a, mod, ctas, stream) : decode_rows<KV_E4M3, 64>(a, mod, ctas, stream);
+    case SDPA_CACHE_INT8: return wide ? decode_rows<KV_INT8, 128>(a, mod, ctas, stream) : decode_rows<KV_INT8, 64>(a, mod, ctas, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace sdpa

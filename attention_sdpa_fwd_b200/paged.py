@@ -24,8 +24,8 @@ from typing import Any, Optional
 
 from . import sdpa_strides_t
 
-PAGED_AUTO, PAGED_EXACT = 0, 1
-PAGED_PATHS = {"auto": PAGED_AUTO, "exact": PAGED_EXACT}
+PAGED_AUTO, PAGED_EXACT, PAGED_DECODE = 0, 1, 2
+PAGED_PATHS = {"auto": PAGED_AUTO, "exact": PAGED_EXACT, "decode": PAGED_DECODE}
 CACHE_F32, CACHE_BF16, CACHE_E4M3, CACHE_INT8 = 0, 1, 2, 3
 
 
@@ -59,7 +59,7 @@ def bind(L) -> None:
     L.sdpa_cache_write.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp]
     L.sdpa_cache_read.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp]
     L.sdpa_fwd_paged.argtypes = [_vp] * 6 + [_i32, _i32, _f32, _i32, _f32, _vp, _vp, _i32, _vp, _i64, _vp]
-    L.sdpa_fwd_paged_workspace.argtypes = [_vp, _vp, _i32, _i32, _i32]
+    L.sdpa_fwd_paged_workspace.argtypes = [_vp] * 6 + [_i32, _i32, _i32]
     for n in ("sdpa_cache_write", "sdpa_cache_read", "sdpa_fwd_paged"):
         getattr(L, n).restype = _i32
     L.sdpa_fwd_paged_workspace.restype = _i64
@@ -87,8 +87,9 @@ def sdpa_fwd_paged(q, q_strides, cache, batch, out, out_strides, dtype, Hq, scal
                                      scale, window, softcap, slopes, lse, path, workspace, workspace_bytes, stream)
 
 
-def sdpa_fwd_paged_workspace(cache, batch, dtype, Hq, path) -> int:
-    return _S().lib().sdpa_fwd_paged_workspace(_ref(cache), _ref(batch), dtype, Hq, path)
+def sdpa_fwd_paged_workspace(cache, batch, q, q_strides, out, out_strides, dtype, Hq, path) -> int:
+    return _S().lib().sdpa_fwd_paged_workspace(_ref(cache), _ref(batch), q, _ref(q_strides), out, _ref(out_strides),
+                                               dtype, Hq, path)
 
 
 # ---------------------------------------------------------------------------
@@ -292,7 +293,7 @@ def sdpa_paged(q, cache: KVCache, page_table, kv_lens, cu_q=None, scale: Optiona
             raise ValueError("out must have q's shape and dtype")
         os_ = _rows(out, Hq, d, "out", cache.k)
         desc, code = cache.descriptor(), S._dtype_code(q)
-        need = sdpa_fwd_paged_workspace(desc, batch, code, Hq, PAGED_PATHS[path])
+        need = sdpa_fwd_paged_workspace(desc, batch, q.data_ptr(), qs, out.data_ptr(), os_, code, Hq, PAGED_PATHS[path])
         _check(min(need, 0), "sdpa_fwd_paged_workspace")
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         _check(sdpa_fwd_paged(q.data_ptr(), qs, desc, batch, out.data_ptr(), os_, code, Hq,

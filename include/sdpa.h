@@ -373,7 +373,10 @@ int sdpa_cache_read(const sdpa_cache_t* cache, const sdpa_batch_t* batch, void* 
 /* Kernel families of sdpa_fwd_paged. */
 typedef enum {
   SDPA_PAGED_AUTO = 0,
-  SDPA_PAGED_EXACT = 1  /* CUDA cores, fp32 arithmetic; every type, layout and option */
+  SDPA_PAGED_EXACT = 1,  /* CUDA cores, fp32 arithmetic; every type, layout and option */
+  SDPA_PAGED_DECODE = 2  /* few new rows (max_q * Hq / Hkv <= 32): mma.sync, the keys of the whole batch
+                            divided evenly over the SMs; BF16 I/O, d 64 or 128, page_size a multiple of
+                            16, 16-byte aligned rows of q and the cache */
 } sdpa_paged_path_t;
 
 /*
@@ -403,10 +406,13 @@ int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const sdpa_cache
                float softcap, const float* slopes, float* lse, int path, void* workspace, int64_t workspace_bytes,
                cudaStream_t stream);
 
-/* Bytes of scratch sdpa_fwd_paged needs for calls of these sizes (0: none), or a
-   negative sdpa_status.  Looks at the sizes, strides and alignment only,
-   launches nothing. */
-int64_t sdpa_fwd_paged_workspace(const sdpa_cache_t* cache, const sdpa_batch_t* batch, sdpa_dtype_t dtype, int Hq, int path);
+/* Bytes of scratch sdpa_fwd_paged needs for a call with these arguments (0:
+   none), or a negative sdpa_status.  Looks at sizes, strides, alignment and
+   the spans of the pointers only, launches nothing; the answer holds for every
+   call whose arguments differ in the addresses of equally aligned buffers. */
+int64_t sdpa_fwd_paged_workspace(const sdpa_cache_t* cache, const sdpa_batch_t* batch, const void* q,
+                                 const sdpa_rows_t* q_strides, const void* out, const sdpa_rows_t* out_strides,
+                                 sdpa_dtype_t dtype, int Hq, int path);
 
 /* Synchronises `stream`, then returns and clears the device error word of the
    current device: SDPA_OK; SDPA_ERR_DEVICE_INDEX when a paged operator met a

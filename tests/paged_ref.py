@@ -86,7 +86,7 @@ class Pool:
         return self.val[which][self.table[b, j // self.page].long(), :, j % self.page].transpose(0, 1)
 
 
-def attend(pool, q, n, *, scale=None, window=0, softcap=0.0, slopes=None, u_p=0.0):
+def attend(pool, q, n, *, scale=None, window=0, softcap=0.0, slopes=None, u_p=0.0, p_floor=0.0):
     """(out, lse, bound on |out|'s error without its own rounding, bound on
     lse's) in 64 bits for packed rows q [sum n, Hq, d].
 
@@ -94,7 +94,14 @@ def attend(pool, q, n, *, scale=None, window=0, softcap=0.0, slopes=None, u_p=0.
     twice a rounding each: tensor cores may cut instead of rounding), of
     the few operations behind them and of exp2 (2^-22); a weight is off by a
     factor e^(+-e) and by u_p where P is rounded; the value sum adds its own
-    accumulation, one rounding per 8 keys and a few."""
+    accumulation, one rounding per 8 keys and a few.
+
+    p_floor: where P is f16 a weight below f16's normal range is off by half
+    its smallest number whatever its size.  In units of P that is 2^-25, with
+    the largest P at 2^12 or more: 2^-37 of the largest.  P there stands for
+    2^t, t_j = x_j log2 e + log2 vs_j, and multiplies codes c_j, so the sum of
+    p_j c_j is off by at most p_floor 2^tmax sum |c_j|; it is divided by sum
+    2^t_j / vs_j >= 2^tmax / vs_(argmax t): p_floor vs_(argmax t) sum |c_j|."""
     T, Hq, d = q.shape
     q = q.double()
     scale = 1.0 / math.sqrt(d) if scale is None else scale
@@ -134,6 +141,11 @@ def attend(pool, q, n, *, scale=None, window=0, softcap=0.0, slopes=None, u_p=0.
                 pe = p * (2 * e)
                 acc = (L / 8 + 64) * 2.0 ** -23
                 tol[at:at + m, h] = (pe + (u_p + acc) * p) @ vv.abs() + (pe.sum(-1, keepdim=True) + acc) * out[at:at + m, h].abs()
+                if p_floor:
+                    vs = pool.scales[1].double()[pool.table[b, j[0] // pool.page].long(), h // G, j[0] % pool.page]
+                    t = x / math.log(2.0) + vs.log2()
+                    size_c = (~hidden).double() @ (vv / vs[:, None]).abs()
+                    tol[at:at + m, h] += p_floor * vs[t.argmax(-1)][:, None] * size_c
                 ltol[at:at + m, h] = pe.sum(-1) + acc + 2.0 ** -22 * lse[at:at + m, h].abs().nan_to_num(posinf=0)
         at += m
     return out, lse, tol, ltol

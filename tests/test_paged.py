@@ -144,8 +144,11 @@ def run_case(path, cdt, io, Hq, Hkv, d, page, kv, n, *, layout="hnd", window=0, 
                        scale, max_q=max(rows + [0]), window=window, softcap=softcap,
                        slopes=None if sl is None else sl.cuda(), lse=lse, path=path, **kw)
     assert device_error() == 0
-    u_p = 0.0 if path == "exact" or io == F32 else R.U[torch.float16 if cdt in R.QMAX else BF16]
-    want, wlse, tol, ltol = R.attend(pool, q, rows, scale=scale, window=window, softcap=softcap, slopes=sl, u_p=u_p)
+    codes = cdt in R.QMAX
+    rounded = path != "exact" and io == BF16  # P is f16 beside codes, else bf16
+    want, wlse, tol, ltol = R.attend(pool, q, rows, scale=scale, window=window, softcap=softcap, slopes=sl,
+                                     u_p=R.U[torch.float16 if codes else BF16] if rounded else 0.0,
+                                     p_floor=2.0 ** -37 if rounded and codes else 0.0)
     what = f"{path} {cdt} {Hq}/{Hkv} d{d} page {page} kv {kv} n {n} w{window} c{softcap} s{slopes}"
     R.check(out, want, tol, io, what)
     R.check_lse(lse, wlse, ltol, what)
@@ -173,3 +176,52 @@ def test_exact_options(cdt, kw):
 def test_exact_more_rows_than_tokens():
     """New rows in front of the sequence's first token see nothing: zero, -inf."""
     run_case("exact", BF16, BF16, 4, 2, 64, 16, [3, 0, 20], [5, 2, 4])
+
+
+# lengths around the tiles (64 or 128 keys to a CTA's tile, 16 or 32 to a warp's step), one sequence and many
+DECODE_LENS = [[1], [2, 15, 16, 17], [31, 33, 63, 64, 65], [127, 128, 129, 500], [3000, 1, 0, 777], [9000]]
+
+
+@pytest.mark.parametrize("kv", DECODE_LENS, ids=str)
+@pytest.mark.parametrize("cdt", [BF16, E4M3, INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_lengths(d, cdt, kv):
+    run_case("decode", cdt, BF16, 8, 2, d, 16, kv, None, seed=len(kv))
+
+
+@pytest.mark.parametrize("Hq,Hkv,n", [(1, 1, [1, 1, 1]), (32, 1, [1, 1, 1]), (7, 1, [2, 1, 2]), (12, 12, [9, 1, 16]),
+                                      (24, 3, [4, 2, 3]), (6, 2, [5, 0, 10]), (16, 1, [1, 2, 1]), (32, 2, [1, 0, 1])])
+@pytest.mark.parametrize("cdt", [BF16, E4M3, INT8])
+@pytest.mark.parametrize("d,page,layout", [(128, 48, "hnd"), (64, 32, "nhd")])
+def test_decode_rows(d, page, layout, cdt, Hq, Hkv, n):
+    run_case("decode", cdt, BF16, Hq, Hkv, d, page, [700, 20, 260], n, layout=layout, seed=Hq)
+
+
+OPTIONS = [dict(window=1), dict(window=17), dict(window=100), dict(window=100000), dict(softcap=5.0), dict(slopes=True),
+           dict(window=200, softcap=20.0, slopes=True), dict(scale=0.0), dict(scale=-0.3), dict(qstd=30.0)]
+
+
+@pytest.mark.parametrize("kw", OPTIONS, ids=str)
+@pytest.mark.parametrize("n", [[1, 1, 1], [6, 3, 8]], ids=str)
+@pytest.mark.parametrize("cdt", [BF16, E4M3, INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_options(d, cdt, n, kw):
+    run_case("decode", cdt, BF16, 8, 4, d, 16, [1000, 131, 64], n, seed=d, **kw)
+
+
+def test_decode_many_sequences():
+    """More sequences than a CTA has threads, most of them empty or short."""
+    kv = [(i * 37) % 90 if i % 3 else 0 for i in range(300)]
+    run_case("decode", BF16, BF16, 4, 2, 64, 16, kv, [1 if i % 5 else 0 for i in range(300)])
+
+
+def test_decode_more_rows_than_tokens():
+    run_case("decode", E4M3, BF16, 4, 2, 64, 16, [3, 0, 200], [5, 2, 4])
+
+
+@pytest.mark.parametrize("cdt", [BF16, INT8])
+def test_decode_equals_itself_and_any_split(cdt):
+    """The same call twice gives the same bits."""
+    a = run_case("decode", cdt, BF16, 8, 2, 128, 16, [5000, 300], None)
+    b = run_case("decode", cdt, BF16, 8, 2, 128, 16, [5000, 300], None)
+    assert torch.equal(a, b)
