@@ -109,9 +109,10 @@ __device__ __forceinline__ void seen(const PagedParams& p, int pos, int& lo, int
 
 // Code pairs to f16 pairs (exact): two e4m3 in the low 16 bits; two signed
 // bytes u0, u1 as f16 1024 + (u ^ 128) minus 1152.
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(w));
 }
 // bytes at selectors 0..3 of x ^ 0x80808080 already applied by the caller
 __device__ __forceinline__ uint32_t biased_bytes_to_half2(uint32_t x, uint32_t sel) {

@@ -221,8 +221,7 @@ extern "C" int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const
   const Plan plan = make_plan(p, dtype, path);
   if (plan.status != SDPA_OK) return plan.status;
   if (plan.ws_bytes > 0) {
-    if (workspace == nullptr) return SDPA_ERR_INVALID_ARG;
-    if (workspace_bytes < plan.ws_bytes) return SDPA_ERR_CAPACITY;
+    if (workspace == nullptr || workspace_bytes < plan.ws_bytes) return SDPA_ERR_CAPACITY;
     if (!aligned_to(workspace, 16)) return SDPA_ERR_MISALIGNED;
   }
   if (plan.decode && launch_paged_decode(p, workspace, stream) != cudaSuccess) return SDPA_ERR_CUDA;

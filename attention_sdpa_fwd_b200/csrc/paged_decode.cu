@@ -36,6 +36,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "paged.cuh"
 #include "pdl_launch.cuh"
 #include "softmax_tile.cuh"
@@ -76,12 +78,14 @@ struct Cfg {
   static constexpr int kTile = KS * kRow;                               // K (or V) of a step
   static constexpr int kScales = KV == KV_BF16 ? 0 : 4 * KS * 4;        // ks, vs, log2 vs, 1 / vs
   static constexpr int kStage = 2 * kTile + kScales;
-  static constexpr int NST = KV != KV_BF16 && D == 64 ? 5 : 3;
+  static constexpr bool kQSmem = MT > 1 || KV != KV_BF16;               // Q fragments in shared memory
+  static constexpr int kCtas = MT == 1 && KV != KV_BF16 ? 3 : 2;        // of an SM
+  static constexpr int NST = KV == KV_BF16 ? 3 : MT > 1 ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 3);
   static constexpr int kRows = 16 * MT;
   static constexpr int kPitch = D + 4;
   static constexpr int kRing = kWarps * NST * kStage;
   static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
-  static constexpr int kQ = MT > 1 ? MT * (D / 16) * 32 * 16 : 0;       // Q fragments in shared memory
+  static constexpr int kQ = kQSmem ? MT * (D / 16) * 32 * 16 : 0;
   static constexpr int kBig = kRing > kMergeBytes ? kRing : kMergeBytes;
   static constexpr int oQ = kBig;
   static constexpr int oML = oQ + kQ;                                   // [kWarps][kRows] float2
@@ -133,8 +137,7 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 template <int KV>
 __device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (KV == KV_E4M3) {
-    lo = e4m3x2_to_half2(w & 0xffffu);
-    hi = e4m3x2_to_half2(w >> 16);
+    e4m3x4_to_half2(w, lo, hi);
   } else {
     w ^= 0x80808080u;
     lo = biased_bytes_to_half2(w, 0x4140);
@@ -177,11 +180,16 @@ __device__ __forceinline__ Unit unit_of(const DecodeArgs& a, int b) {
   return u;
 }
 
+// a / b, mostly of numbers that fit 32 bits
+__device__ __forceinline__ long long div64(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // CTA that owns tile f of T split over G
-__device__ __forceinline__ int owner(long long f, long long T, int G) { return (int)(((f + 1) * G - 1) / T); }
+__device__ __forceinline__ int owner(long long f, long long T, int G) { return (int)div64((f + 1) * G - 1, T); }
 
 template <int KV, int D, int MT, bool MOD>
-__global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decode_kernel(const __grid_constant__ DecodeArgs a) {
   using C = Cfg<KV, D, MT>;
   constexpr bool F16 = KV != KV_BF16;
   constexpr int KS = C::KS, SB = C::SB, NST = C::NST;
@@ -230,8 +238,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
     T = total * p.c.Hkv;
     // at least two tiles to a CTA
     work_ctas = (int)min((long long)G, max(1LL, T / 2));
-    cur = blockIdx.x < work_ctas ? T * blockIdx.x / work_ctas : T;
-    end = blockIdx.x < work_ctas ? T * (blockIdx.x + 1) / work_ctas : T;
+    cur = blockIdx.x < work_ctas ? div64(T * blockIdx.x, work_ctas) : T;
+    end = blockIdx.x < work_ctas ? div64(T * (blockIdx.x + 1), work_ctas) : T;
     long long at = (incl - mine) * p.c.Hkv;
     if (cur < end && cur >= at && cur < at + mine * p.c.Hkv) {
       int bb = tid * per;
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
   while (cur < end && b < p.s.B) {
     const Unit u = unit_of<C::kKeys>(a, b);
     if (u.nt == 0) { ++b; continue; }
-    const int hk = (int)((cur - F) / u.nt);
+    const int hk = (int)div64(cur - F, u.nt);
     const int tile0 = (int)((cur - F) - (long long)hk * u.nt);
     const int ntile = (int)min((long long)(u.nt - tile0), end - cur);
     const int base = u.lo16 + tile0 * C::kKeys + warp * KS;  // this warp's first key
@@ -269,42 +277,63 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
     // ---- the ring: one step is KS keys and values of this warp
     const uint8_t* kp = static_cast<const uint8_t*>(p.c.k) + (long long)hk * p.c.kh * C::kElem;
     const uint8_t* vp = static_cast<const uint8_t*>(p.c.v) + (long long)hk * p.c.vh * C::kElem;
-    int pg[KS / 16];
+    constexpr int kPieces = C::kRow / 16;  // of a row
+    constexpr int kPass = 32 / kPieces;    // rows the warp copies at once
+    const int piece = lane % kPieces, r0 = lane / kPieces;
+    const long long kstep = p.c.kt * (kPass * C::kElem), vstep = p.c.vt * (kPass * C::kElem);
+    kp += (long long)r0 * p.c.kt * C::kElem + piece * 16;
+    vp += (long long)r0 * p.c.vt * C::kElem + piece * 16;
+    // the next step's pages: where this lane's first row of each 16 tokens is
+    const uint8_t *kq[KS / 16], *vq[KS / 16];
+    const float *ksq, *vsq;
+    // Page numbers are fetched 32 sixteen-token groups at a time, a lane per
+    // group, one such span ahead of its use.
+    constexpr int kGroups = KS / 16, kSpan = 32 / kGroups;
+    auto fetch = [&](int span) {
+      const int step = span * kSpan + lane / kGroups;
+      const int t = base + step * C::kKeys + 16 * (lane % kGroups);
+      return step < ntile && t < khi && t + 16 > klo ? page_of(p.s, p.c, b, t, p.err) : 0;
+    };
+    int pages = fetch(0), pages_next = fetch(1);
+    // where this lane's first row of each 16 tokens of a step is
     auto lookup = [&](int step) {
+      if (step > 0 && step % kSpan == 0) {
+        pages = pages_next;
+        pages_next = fetch(step / kSpan + 1);
+      }
       const int t0 = base + step * C::kKeys;
 #pragma unroll
-      for (int g = 0; g < KS / 16; ++g) {
+      for (int g = 0; g < kGroups; ++g) {
         const int t = t0 + 16 * g;
-        pg[g] = step < ntile && t < khi && t + 16 > klo ? page_of(p.s, p.c, b, t, p.err) : 0;
+        const long long pg = __shfl_sync(0xffffffffu, pages, (step % kSpan) * kGroups + g);
+        const int off = t - (int)fdiv((uint32_t)t, p.c.fd_page) * p.c.page_size;
+        kq[g] = kp + (pg * p.c.kp + off * p.c.kt) * C::kElem;
+        vq[g] = vp + (pg * p.c.vp + off * p.c.vt) * C::kElem;
+        if (F16 && lane / 16 == g) {
+          ksq = p.c.ks + pg * p.c.ksp + hk * p.c.ksh + (off + lane % 16) * p.c.kst;
+          vsq = p.c.vs + pg * p.c.vsp + hk * p.c.vsh + (off + lane % 16) * p.c.vst;
+        }
       }
     };
     auto issue = [&](int step) {
       if (step < ntile) {
-        constexpr int kPieces = C::kRow / 16;     // of a row
-        constexpr int kPass = 32 / kPieces;       // rows of a pass
         const uint32_t st = ring + (step % NST) * C::kStage;
         const int t0 = base + step * C::kKeys;
-        const int piece = lane % kPieces, r0 = lane / kPieces;
+        const bool all = t0 >= klo && t0 + KS <= khi;
 #pragma unroll
         for (int i = 0; i < KS / kPass; ++i) {
-          const int r = i * kPass + r0;
-          const int g = (i * kPass) / 16;
-          const int t = t0 + r;
-          const bool live = t >= klo && t < khi;
-          const int off = live ? t - (int)fdiv((uint32_t)t, p.c.fd_page) * p.c.page_size : 0;
-          const uint8_t* ks = kp + ((long long)pg[g] * p.c.kp + (long long)off * p.c.kt) * C::kElem + piece * 16;
-          const uint8_t* vs = vp + ((long long)pg[g] * p.c.vp + (long long)off * p.c.vt) * C::kElem + piece * 16;
-          cp16(st + k_off<KV, D>(r, piece), ks, live);
-          cp16(st + C::kTile + v_off<KV, D>(r, piece), vs, live);
+          const int r = i * kPass + r0, g = (i * kPass) / 16;
+          const bool live = all || (t0 + r >= klo && t0 + r < khi);
+          cp16(st + k_off<KV, D>(r, piece), kq[g], live);
+          cp16(st + C::kTile + v_off<KV, D>(r, piece), vq[g], live);
+          kq[g] += kstep;
+          vq[g] += vstep;
         }
-        if constexpr (F16) {
-          const int t = t0 + lane;  // KS == 32
-          const bool live = t >= klo && t < khi;
-          const int off = live ? t - (int)fdiv((uint32_t)t, p.c.fd_page) * p.c.page_size : 0;
-          const long long pl = lane < 16 ? pg[0] : pg[KS / 16 - 1];
+        if constexpr (F16) {  // KS == 32: a lane per key
+          const bool live = all || (t0 + lane >= klo && t0 + lane < khi);
           const uint32_t sc = st + 2 * C::kTile + lane * 4;
-          cp4(sc, p.c.ks + pl * p.c.ksp + hk * p.c.ksh + off * p.c.kst, live);
-          cp4(sc + KS * 4, p.c.vs + pl * p.c.vsp + hk * p.c.vsh + off * p.c.vst, live);
+          cp4(sc, ksq, live);
+          cp4(sc + KS * 4, vsq, live);
         }
       }
       cp_commit();
@@ -317,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
     lookup(NST - 1);
 
     // ---- Q as A fragments: row r of the unit is token r / group, head r % group
-    uint32_t qf[MT == 1 ? D / 16 : 1][4];
+    uint32_t qf[C::kQSmem ? 1 : D / 16][4];
     float xscale[MT][2];  // what turns the accumulator of a row into its score
     int pos[MT][2];
     float slope[MT][2];
@@ -366,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
         // pair 2s is a0 / a1 of k-step s, pair 2s + 1 is a2 / a3
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          if constexpr (MT == 1) {
+          if constexpr (!C::kQSmem) {
             qf[s][e] = w[2 * s];
             qf[s][2 + e] = w[2 * s + 1];
           } else if (s % kWarps == warp) {  // every warp has the same fragments: each writes a share
@@ -376,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
         }
       }
     }
-    if constexpr (MT > 1) __syncthreads();
+    if constexpr (C::kQSmem) __syncthreads();
 
     float o[MT][D / 8][4];
     float mx[MT][2], l[MT][2];
@@ -433,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
 #pragma unroll
           for (int ss = 0; ss < D / 16; ++ss) {
             uint32_t q4[MT][4];
-            if constexpr (MT > 1) {
+            if constexpr (C::kQSmem) {
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
                 const uint4 x = lds16(smem_u32(smem) + C::oQ + ((m * (D / 16) + ss) * 32 + lane) * 16);
@@ -446,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
               codes4<KV>(w[n][ss], b0, b1);
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
-                if constexpr (MT > 1) mma<F16>(s[m][n], q4[m], b0, b1);
+                if constexpr (C::kQSmem) mma<F16>(s[m][n], q4[m], b0, b1);
                 else mma<F16>(s[m][n], qf[ss], b0, b1);
               }
             }
@@ -513,12 +542,22 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
               } else {
                 x = s[m][n][k] * (xscale[m][e] * kLog2e);
               }
-              if (edge && (j > pos[m][e] || (p.window > 0 && j <= pos[m][e] - p.window)))
-                x = -INFINITY;
               s[m][n][k] = x;
-              top[e] = fmaxf(top[e], x);
             }
           }
+          if (edge) {
+#pragma unroll
+            for (int n = 0; n < SB / 8; ++n)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int j = t0 + sb + n * 8 + 2 * c + (k & 1);
+                if (j > pos[m][k >> 1] || (p.window > 0 && j <= pos[m][k >> 1] - p.window)) s[m][n][k] = -INFINITY;
+              }
+          }
+#pragma unroll
+          for (int n = 0; n < SB / 8; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top[k >> 1] = fmaxf(top[k >> 1], s[m][n][k]);
           bool grow = false;
           float al[2];
 #pragma unroll
@@ -709,9 +748,10 @@ __global__ void __launch_bounds__(kThreads) paged_merge_kernel(const __grid_cons
   const long long f = a.ws_first[blockIdx.x];
   const int c0 = owner(f, T, G), c1 = owner(f + u.nt - 1, T, G);
   if (c0 == c1) return;
+  const long long first0 = div64(T * c0, G);  // c0's first tile
   for (int i = threadIdx.x; i < u.rows * (D / 4); i += kThreads) {
     const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
-    auto slot = [&](int cta) { return 2LL * cta + (cta == c0 && f > T * c0 / G ? 1 : 0); };
+    auto slot = [&](int cta) { return 2LL * cta + (cta == c0 && f > first0 ? 1 : 0); };
     float top = -INFINITY, den = 0.f;
     for (int q = c0; q <= c1; ++q) top = fmaxf(top, a.ws_ml[slot(q) * ROWS + r].x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -737,11 +777,25 @@ __global__ void __launch_bounds__(kThreads) paged_merge_kernel(const __grid_cons
   }
 }
 
+// Raises a kernel's shared-memory limit once per device (`done`: a bit each).
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 template <int KV, int D, int MT>
 cudaError_t decode_one(DecodeArgs& a, bool mod, int ctas, cudaStream_t stream) {
   using C = Cfg<KV, D, MT>;
   auto kern = mod ? paged_decode_kernel<KV, D, MT, true> : paged_decode_kernel<KV, D, MT, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
+  static std::atomic<uint64_t> done[2];
+  cudaError_t e = allow_smem(kern, C::kTotal, done[mod]);
   if (e != cudaSuccess) return e;
   e = launch_serialized(kern, dim3((unsigned)ctas), dim3(kThreads), (size_t)C::kTotal, stream, a);
   if (e != cudaSuccess || a.whole) return e;
@@ -762,6 +816,11 @@ int row_limit(const PagedParams& p) { return (long long)p.s.max_q * p.group <= 1
 bool whole_units(const PagedParams& p) {
   const int tile = p.c.dtype == SDPA_CACHE_BF16 && p.c.d == 128 ? 64 : 128;
   return (long long)p.s.max_pages * p.c.page_size <= 2 * tile;
+}
+
+// One resident wave.
+int decode_ctas(const PagedParams& p) {
+  return num_sms() * (p.c.dtype != SDPA_CACHE_BF16 && row_limit(p) == 16 ? 3 : 2);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -785,7 +844,7 @@ int paged_decode_check(const PagedParams& p, sdpa_dtype_t dtype) {
 
 size_t paged_decode_workspace(const PagedParams& p) {
   if (whole_units(p) || p.s.total_q == 0) return 0;
-  const size_t slots = 2 * 2 * (size_t)num_sms(), rows = row_limit(p);
+  const size_t slots = 2 * (size_t)decode_ctas(p), rows = row_limit(p);
   return up256(slots * rows * p.c.d * 4) + up256(slots * rows * 8) + up256((size_t)p.s.B * p.c.Hkv * 8) + 256;
 }
 
@@ -795,7 +854,7 @@ cudaError_t launch_paged_decode(const PagedParams& p, void* ws, cudaStream_t str
   a.p = p;
   a.limit = row_limit(p);
   a.whole = whole_units(p);
-  const int ctas = a.whole ? p.s.B * p.c.Hkv : 2 * num_sms();
+  const int ctas = a.whole ? p.s.B * p.c.Hkv : decode_ctas(p);
   if (!a.whole) {
     const size_t slots = 2 * (size_t)ctas, rows = a.limit;
     char* w = static_cast<char*>(ws);

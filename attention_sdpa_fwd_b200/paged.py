@@ -19,8 +19,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
-from dataclasses import dataclass
-from typing import Any, Optional
+from typing import Optional
 
 from . import sdpa_strides_t
 
@@ -104,33 +103,42 @@ def _cache_code(dtype) -> int:
     return codes[dtype]
 
 
-@dataclass
 class KVCache:
     """A pool of pages: ``k`` and ``v`` [num_pages, Hkv, page_size, d] CUDA
     tensors of one dtype with a contiguous last axis (any other strides: a pool
     laid out [num_pages, page_size, Hkv, d] is passed as its transpose(1, 2)).
     float8_e4m3fn and int8 pools also have float32 ``k_scale`` and ``v_scale``
-    [num_pages, Hkv, page_size]."""
-    k: Any
-    v: Any
-    k_scale: Any = None
-    v_scale: Any = None
+    [num_pages, Hkv, page_size].  The tensors of a cache do not change."""
 
-    def __post_init__(self):
+    def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
-        code = _cache_code(self.k.dtype)
-        for t in (self.k, self.v):
-            if t.dim() != 4 or t.shape != self.k.shape or t.dtype != self.k.dtype or t.device != self.k.device:
+        code = _cache_code(k.dtype)
+        for t in (k, v):
+            if t.dim() != 4 or t.shape != k.shape or t.dtype != k.dtype or t.device != k.device:
                 raise ValueError("k and v must be [num_pages, Hkv, page_size, d] of one shape, dtype and device")
             if t.stride(3) != 1:
                 raise ValueError("k and v must have a contiguous last axis")
-        scales = (self.k_scale, self.v_scale)
         if code in (CACHE_E4M3, CACHE_INT8):
-            for t in scales:
-                if t is None or t.shape != self.k.shape[:3] or t.dtype != torch.float32 or t.device != self.k.device:
+            for t in (k_scale, v_scale):
+                if t is None or t.shape != k.shape[:3] or t.dtype != torch.float32 or t.device != k.device:
                     raise ValueError("an 8-bit cache needs float32 k_scale and v_scale [num_pages, Hkv, page_size]")
-        elif any(t is not None for t in scales):
+        elif k_scale is not None or v_scale is not None:
             raise ValueError("only 8-bit caches have scales")
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
+        self.Hkv, self.page_size, self.d = k.shape[1:]
+        self.device = k.device
+        c = sdpa_cache_t(k=k.data_ptr(), v=v.data_ptr(), dtype=code, num_pages=k.shape[0], Hkv=self.Hkv,
+                         page_size=self.page_size, d=self.d, k_strides=_strides(k), v_strides=_strides(v))
+        if k_scale is not None:
+            c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+            c.k_scale_strides, c.v_scale_strides = _strides(k_scale), _strides(v_scale)
+        self._descriptor = c
+        self._workspace = 0  # bytes the last sdpa_paged needed: where the next one starts from
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, Hkv: int, d: int, dtype, device="cuda") -> "KVCache":
@@ -143,60 +151,82 @@ class KVCache:
         return cls(k, v)
 
     def descriptor(self) -> sdpa_cache_t:
-        # a one-page, one-head or one-token axis may carry any stride: it is never stepped
-        def st(t):
-            return sdpa_strides_t(*(max(1, t.stride(i)) if t.shape[i] == 1 else t.stride(i) for i in range(3)))
-        c = sdpa_cache_t(k=self.k.data_ptr(), v=self.v.data_ptr(), dtype=_cache_code(self.k.dtype),
-                         num_pages=self.k.shape[0], Hkv=self.k.shape[1], page_size=self.k.shape[2], d=self.k.shape[3],
-                         k_strides=st(self.k), v_strides=st(self.v))
-        if self.k_scale is not None:
-            c.k_scale, c.v_scale = self.k_scale.data_ptr(), self.v_scale.data_ptr()
-            c.k_scale_strides, c.v_scale_strides = st(self.k_scale), st(self.v_scale)
-        return c
+        """The C structure of the pool."""
+        return self._descriptor
+
+
+def _strides(t) -> sdpa_strides_t:
+    """Of the first three axes; an axis of one element is never stepped, so it
+    may carry any stride."""
+    return sdpa_strides_t(*(max(1, s) if n == 1 else s for s, n in zip(t.stride()[:3], t.shape[:3])))
 
 
 def _batch(cache: KVCache, page_table, kv_lens, cu_q, total_q: int, max_q: Optional[int]) -> sdpa_batch_t:
     import torch
-    dev = cache.k.device
+    dev = cache.device
     for t, dim, name in ((page_table, 2, "page_table"), (kv_lens, 1, "kv_lens"), (cu_q, 1, "cu_q")):
         if t is None and name == "cu_q":
             continue
         if t.dtype != torch.int32 or t.dim() != dim or t.device != dev:
             raise ValueError(f"{name} must be a {dim}-D int32 tensor on the cache's device")
-        if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
             raise ValueError(f"{name} must have a contiguous last axis")
-    B = kv_lens.shape[0]
+    B, width = kv_lens.shape[0], page_table.shape[1]
     if page_table.shape[0] != B or (cu_q is not None and cu_q.shape[0] != B + 1):
         raise ValueError("page_table must be [B, max_pages], kv_lens [B], cu_q [B + 1]")
     if cu_q is None and total_q != B:
         raise ValueError("without cu_q there is one new row per sequence")
-    if max_q is not None and max_q < 0:
+    if max_q is None:
+        max_q = total_q
+    elif max_q < 0:
         raise ValueError("max_q must not be negative")
-    width = page_table.shape[1]
-    return sdpa_batch_t(page_table=page_table.data_ptr(), table_stride=page_table.stride(0) if B > 1 else width,
-                        max_pages=width, kv_lens=kv_lens.data_ptr(), cu_q=None if cu_q is None else cu_q.data_ptr(),
-                        B=B, total_q=total_q, max_q=total_q if max_q is None else min(int(max_q), 0x7fffffff))
+    return sdpa_batch_t(page_table.data_ptr(), page_table.stride(0) if B > 1 else width, width, kv_lens.data_ptr(),
+                        None if cu_q is None else cu_q.data_ptr(), B, total_q, min(int(max_q), 0x7fffffff))
 
 
-def _rows(t, heads: int, d: int, name: str, like) -> sdpa_rows_t:
-    if not t.is_cuda or t.device != like.device:
+def _rows(t, heads: int, cache: KVCache, name: str) -> Optional[sdpa_rows_t]:
+    """Strides of packed rows (None: dense), checked."""
+    if t.device != cache.device or not t.is_cuda:
         raise ValueError(f"{name} must be on the cache's CUDA device (no CPU fallback)")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [tokens, {heads}, {d}] with a contiguous last axis")
-    return sdpa_rows_t(t.stride(0) if t.shape[0] > 1 else max(1, t.stride(0)), t.stride(1) if heads > 1 else max(1, t.stride(1)))
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {cache.d}]")
+    if t.is_contiguous():
+        return None
+    n, h, d = t.stride()
+    if d != 1:
+        raise ValueError(f"{name} must have a contiguous last axis")
+    return sdpa_rows_t(n if t.shape[0] > 1 else max(1, n), h if heads > 1 else max(1, h))
 
 
 @contextlib.contextmanager
-def _on(device, stream):
-    """The tensors' device, and the stream asked for, current: what a call
-    allocates belongs to the stream its kernels run on."""
+def _switch(device, stream):
     import torch
     with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device)
-        else:
-            with torch.cuda.stream(stream):
-                yield stream
+        with torch.cuda.stream(stream):
+            yield (stream or torch.cuda.current_stream(device)).cuda_stream
+
+
+class _Here:
+    """The current stream of the current device."""
+
+    def __enter__(self):
+        import torch
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        return False
+
+
+_here = _Here()
+
+
+def _on(device, stream):
+    """The tensors' device, and the stream asked for, current: what a call
+    allocates belongs to the stream its kernels run on.  Gives the handle."""
+    import torch
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _here
+    return _switch(device, stream)
 
 
 def _check(rc: int, what: str) -> None:
@@ -205,7 +235,7 @@ def _check(rc: int, what: str) -> None:
 
 
 def _need_cuda(cache: KVCache) -> None:
-    if not cache.k.is_cuda:
+    if cache.device.type != "cuda":
         raise ValueError("the cache must be on a CUDA device (no CPU fallback)")
 
 
@@ -216,14 +246,13 @@ def cache_write(cache: KVCache, k, v, page_table, kv_lens, cu_q=None, *, max_q: 
     every sequence.  8-bit caches quantise them, one scale per row."""
     S = _S()
     _need_cuda(cache)
-    Hkv, d = cache.k.shape[1], cache.k.shape[3]
-    ks, vs = _rows(k, Hkv, d, "k", cache.k), _rows(v, Hkv, d, "v", cache.k)
+    ks, vs = _rows(k, cache.Hkv, cache, "k"), _rows(v, cache.Hkv, cache, "v")
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must have one shape and dtype")
     batch = _batch(cache, page_table, kv_lens, cu_q, k.shape[0], max_q)
-    with _on(cache.k.device, stream) as st:
-        _check(sdpa_cache_write(cache.descriptor(), batch, k.data_ptr(), ks, v.data_ptr(), vs, S._dtype_code(k),
-                                st.cuda_stream), "sdpa_cache_write")
+    with _on(cache.device, stream) as st:
+        _check(sdpa_cache_write(cache.descriptor(), batch, k.data_ptr(), ks, v.data_ptr(), vs, S._dtype_code(k), st),
+               "sdpa_cache_write")
     return cache
 
 
@@ -236,27 +265,27 @@ def cache_read(cache: KVCache, page_table, kv_lens, k_out=None, v_out=None, *, T
     import torch
     S = _S()
     _need_cuda(cache)
-    B, Hkv, d = kv_lens.shape[0], cache.k.shape[1], cache.k.shape[3]
+    B, Hkv, d = kv_lens.shape[0], cache.Hkv, cache.d
     if (k_out is None) != (v_out is None):
         raise ValueError("give both outputs or none")
     batch = _batch(cache, page_table, kv_lens, None, B, None)
-    with _on(cache.k.device, stream) as st:
+    with _on(cache.device, stream) as st:
         if k_out is None:
             if T is None:
                 raise ValueError("cache_read needs T or outputs")
             dtype = dtype or (torch.float32 if cache.k.dtype == torch.float32 else torch.bfloat16)
-            k_out, v_out = (torch.zeros(B, Hkv, T, d, dtype=dtype, device=cache.k.device) for _ in range(2))
+            k_out, v_out = (torch.zeros(B, Hkv, T, d, dtype=dtype, device=cache.device) for _ in range(2))
         for t in (k_out, v_out):
             if t.dim() != 4 or t.shape != k_out.shape or t.shape[0] != B or t.shape[1] != Hkv or t.shape[3] != d or \
-                    t.stride(3) != 1 or t.dtype != k_out.dtype or t.device != cache.k.device:
+                    t.stride(3) != 1 or t.dtype != k_out.dtype or t.device != cache.device:
                 raise ValueError("outputs must be [B, Hkv, T, d] of one dtype with a contiguous last axis, on the cache's device")
         if T is not None and T != k_out.shape[2]:
             raise ValueError("T differs from the outputs given")
         if dtype is not None and dtype != k_out.dtype:
             raise ValueError("dtype differs from the outputs given")
-        strides = lambda t: sdpa_strides_t(*(max(1, t.stride(i)) if t.shape[i] == 1 else t.stride(i) for i in range(3)))
-        _check(sdpa_cache_read(cache.descriptor(), batch, k_out.data_ptr(), strides(k_out), v_out.data_ptr(),
-                               strides(v_out), S._dtype_code(k_out), k_out.shape[2], st.cuda_stream), "sdpa_cache_read")
+        ks, vs = (None if t.is_contiguous() else _strides(t) for t in (k_out, v_out))
+        _check(sdpa_cache_read(cache.descriptor(), batch, k_out.data_ptr(), ks, v_out.data_ptr(), vs,
+                               S._dtype_code(k_out), k_out.shape[2], st), "sdpa_cache_read")
     return k_out, v_out
 
 
@@ -273,32 +302,42 @@ def sdpa_paged(q, cache: KVCache, page_table, kv_lens, cu_q=None, scale: Optiona
     import torch
     S = _S()
     _need_cuda(cache)
-    d = cache.k.shape[3]
     if q.dim() != 3:
         raise ValueError("q must be [tokens, Hq, d]")
-    Hq = q.shape[1]
-    qs = _rows(q, Hq, d, "q", cache.k)
-    batch = _batch(cache, page_table, kv_lens, cu_q, q.shape[0], max_q)
-    dev = cache.k.device
+    T, Hq, d = q.shape
+    qs = _rows(q, Hq, cache, "q")
+    batch = _batch(cache, page_table, kv_lens, cu_q, T, max_q)
+    dev = cache.device
     if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (Hq,) or not slopes.is_contiguous()
                                or slopes.device != dev):
         raise ValueError("slopes must be a contiguous float32 [Hq] tensor on the cache's device")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (q.shape[0], Hq) or not lse.is_contiguous()
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()
                             or lse.device != dev):
         raise ValueError("lse must be a contiguous float32 [tokens, Hq] tensor on the cache's device")
     with _on(dev, stream) as st:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        elif out.shape != q.shape or out.dtype != q.dtype:
-            raise ValueError("out must have q's shape and dtype")
-        os_ = _rows(out, Hq, d, "out", cache.k)
-        desc, code = cache.descriptor(), S._dtype_code(q)
-        need = sdpa_fwd_paged_workspace(desc, batch, q.data_ptr(), qs, out.data_ptr(), os_, code, Hq, PAGED_PATHS[path])
-        _check(min(need, 0), "sdpa_fwd_paged_workspace")
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        _check(sdpa_fwd_paged(q.data_ptr(), qs, desc, batch, out.data_ptr(), os_, code, Hq,
-                              1.0 / math.sqrt(d) if scale is None else float(scale), int(window), float(softcap),
-                              None if slopes is None else slopes.data_ptr(), None if lse is None else lse.data_ptr(),
-                              PAGED_PATHS[path], None if ws is None else ws.data_ptr(), need, st.cuda_stream),
-               "sdpa_fwd_paged")
+            out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+            os_ = None
+        else:
+            if out.shape != q.shape or out.dtype != q.dtype:
+                raise ValueError("out must have q's shape and dtype")
+            os_ = _rows(out, Hq, cache, "out")
+        desc, code, way = cache.descriptor(), S._dtype_code(q), PAGED_PATHS[path]
+        scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+        qp, op = q.data_ptr(), out.data_ptr()
+        while True:
+            have = cache._workspace
+            ws = torch.empty(have, dtype=torch.uint8, device=dev) if have else None
+            rc = sdpa_fwd_paged(qp, qs, desc, batch, op, os_, code, Hq, scale, int(window), float(softcap),
+                                None if slopes is None else slopes.data_ptr(), None if lse is None else lse.data_ptr(),
+                                way, None if ws is None else ws.data_ptr(), have, st)
+            if rc != -6:
+                break
+            # more scratch than the last call on this cache took
+            need = sdpa_fwd_paged_workspace(desc, batch, qp, qs, op, os_, code, Hq, way)
+            _check(min(need, 0), "sdpa_fwd_paged_workspace")
+            if need <= have:
+                break
+            cache._workspace = need
+        _check(rc, "sdpa_fwd_paged")
     return out

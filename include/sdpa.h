@@ -396,7 +396,7 @@ typedef enum {
  *   path     : sdpa_paged_path_t.
  *   workspace: device scratch of at least sdpa_fwd_paged_workspace() bytes,
  *              16-byte aligned, the call's own until its work on `stream` has
- *              run (SDPA_ERR_CAPACITY when too small).  Nothing is kept in it
+ *              run (SDPA_ERR_CAPACITY when NULL or too small).  Nothing is kept in it
  *              from call to call and it needs no clearing.
  * Values in rows of the cache that the batch's tokens do not cover may be
  * anything; those of V rows it does cover must be finite, seen or not.
