@@ -143,6 +143,10 @@ constexpr int kDecodeRows = 32;
 int paged_decode_check(const PagedParams& p, sdpa_dtype_t dtype);  // SDPA_OK or why it cannot take the layout
 size_t paged_decode_workspace(const PagedParams& p);
 cudaError_t launch_paged_decode(const PagedParams& p, void* ws, cudaStream_t stream);
+// The tensor-core kernel; `limit`: sequences of 1 .. limit rows are left to the decode kernel.
+int paged_tc_check(const PagedParams& p, sdpa_dtype_t dtype);
+size_t paged_tc_workspace(const PagedParams& p, int limit);
+cudaError_t launch_paged_tc(const PagedParams& p, int limit, void* ws, cudaStream_t stream);
 int* error_word();  // device error word of the current device, NULL if it cannot be had
 
 }  // namespace sdpa

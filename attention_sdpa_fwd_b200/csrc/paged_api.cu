@@ -119,18 +119,23 @@ int build_paged(const void* q, const sdpa_rows_t* qs, const sdpa_cache_t* cache,
 }
 
 // Which kernels a call takes.  A sequence's rows per kv head decide: the
-// decode kernel has those of up to kDecodeRows; the host only knows the bound
-// max_q, so a batch that may hold both kinds launches both kernels, and each
-// leaves out the other's sequences.
+// decode kernel has those of up to kDecodeRows, the tensor-core kernel (the
+// exact kernel where a layout keeps that one out) the others.  The host only
+// knows the bound max_q, so a batch that may hold both kinds launches both
+// kernels, and each leaves out the other's sequences; a single sequence that
+// may be long goes to the tensor-core kernel whatever it turns out to be.
 struct Plan {
   int status;
-  bool decode, exact;
+  bool decode, tc, exact;
+  int limit;  // rows up to which sequences are the decode kernel's, for the others
+  size_t decode_ws, tc_ws;
   int64_t ws_bytes;
 };
 
 Plan make_plan(const PagedParams& p, sdpa_dtype_t dtype, int path) {
-  Plan r = {SDPA_OK, false, false, 0};
-  const int dec = paged_decode_check(p, dtype);
+  Plan r;
+  memset(&r, 0, sizeof(r));
+  const int dec = paged_decode_check(p, dtype), tc = paged_tc_check(p, dtype);
   const bool all_few = (long long)p.s.max_q * p.group <= kDecodeRows;
   switch (path) {
     case SDPA_PAGED_EXACT: r.exact = true; break;
@@ -138,11 +143,19 @@ Plan make_plan(const PagedParams& p, sdpa_dtype_t dtype, int path) {
       r.status = dec != SDPA_OK ? dec : all_few ? SDPA_OK : SDPA_ERR_UNSUPPORTED;
       r.decode = true;
       break;
+    case SDPA_PAGED_TCGEN05:
+      r.status = tc;
+      r.tc = true;
+      break;
     default:
-      r.decode = dec == SDPA_OK;
-      r.exact = !r.decode || !all_few;
+      r.decode = dec == SDPA_OK && (all_few || p.s.B > 1 || tc != SDPA_OK);
+      if (!(r.decode && all_few)) (tc == SDPA_OK ? r.tc : r.exact) = true;
   }
-  if (r.decode && r.status == SDPA_OK) r.ws_bytes = (int64_t)paged_decode_workspace(p);
+  if (r.status != SDPA_OK) return r;
+  r.limit = r.decode ? kDecodeRows : 0;
+  if (r.decode) r.decode_ws = (paged_decode_workspace(p) + 255) / 256 * 256;
+  if (r.tc) r.tc_ws = paged_tc_workspace(p, r.limit);
+  r.ws_bytes = (int64_t)(r.decode_ws + r.tc_ws);
   return r;
 }
 
@@ -211,7 +224,7 @@ extern "C" int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const
                           const sdpa_batch_t* batch, void* out, const sdpa_rows_t* out_strides, sdpa_dtype_t dtype,
                           int Hq, float scale, int window, float softcap, const float* slopes, float* lse, int path,
                           void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
-  if (path < SDPA_PAGED_AUTO || path > SDPA_PAGED_DECODE) return SDPA_ERR_INVALID_ARG;
+  if (path < SDPA_PAGED_AUTO || path > SDPA_PAGED_TCGEN05) return SDPA_ERR_INVALID_ARG;
   PagedParams p;
   const int rc = build_paged(q, q_strides, cache, batch, out, out_strides, dtype, Hq, scale, window, softcap, slopes, lse, &p);
   if (rc != SDPA_OK) return rc;
@@ -225,8 +238,10 @@ extern "C" int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const
     if (!aligned_to(workspace, 16)) return SDPA_ERR_MISALIGNED;
   }
   if (plan.decode && launch_paged_decode(p, workspace, stream) != cudaSuccess) return SDPA_ERR_CUDA;
+  if (plan.tc && launch_paged_tc(p, plan.limit, static_cast<char*>(workspace) + plan.decode_ws, stream) != cudaSuccess)
+    return SDPA_ERR_CUDA;
   if (plan.exact) {
-    p.skip_rows = plan.decode ? kDecodeRows : 0;
+    p.skip_rows = plan.limit;
     if (launch_paged_exact(p, dtype, stream) != cudaSuccess) return SDPA_ERR_CUDA;
   }
   return SDPA_OK;
@@ -235,7 +250,7 @@ extern "C" int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const
 extern "C" int64_t sdpa_fwd_paged_workspace(const sdpa_cache_t* cache, const sdpa_batch_t* batch, const void* q,
                                             const sdpa_rows_t* q_strides, const void* out,
                                             const sdpa_rows_t* out_strides, sdpa_dtype_t dtype, int Hq, int path) {
-  if (path < SDPA_PAGED_AUTO || path > SDPA_PAGED_DECODE) return SDPA_ERR_INVALID_ARG;
+  if (path < SDPA_PAGED_AUTO || path > SDPA_PAGED_TCGEN05) return SDPA_ERR_INVALID_ARG;
   PagedParams p;
   const int rc = build_paged(q, q_strides, cache, batch, const_cast<void*>(out), out_strides, dtype, Hq, 1.f, 0, 0.f,
                              nullptr, nullptr, &p);

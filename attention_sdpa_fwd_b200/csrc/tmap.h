@@ -38,7 +38,7 @@ struct TmapKey {
   const void* base;
   uint64_t dims[4];
   uint64_t strides[3];
-  uint32_t box[2];
+  uint32_t box[4];
   int dt, rank, swizzle;
 };
 
@@ -81,8 +81,7 @@ inline TmapKey tmap_key(const void* base, CUtensorMapDataType dt, int rank, cons
   k.base = base;
   for (int i = 0; i < rank; ++i) k.dims[i] = dims[i];
   for (int i = 0; i + 1 < rank; ++i) k.strides[i] = strides[i];
-  k.box[0] = box[0];
-  k.box[1] = box[1];
+  for (int i = 0; i < rank; ++i) k.box[i] = box[i];
   k.dt = (int)dt;
   k.rank = rank;
   k.swizzle = swizzle;

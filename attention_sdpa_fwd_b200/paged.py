@@ -23,8 +23,8 @@ from typing import Optional
 
 from . import sdpa_strides_t
 
-PAGED_AUTO, PAGED_EXACT, PAGED_DECODE = 0, 1, 2
-PAGED_PATHS = {"auto": PAGED_AUTO, "exact": PAGED_EXACT, "decode": PAGED_DECODE}
+PAGED_AUTO, PAGED_EXACT, PAGED_DECODE, PAGED_TCGEN05 = 0, 1, 2, 3
+PAGED_PATHS = {"auto": PAGED_AUTO, "exact": PAGED_EXACT, "decode": PAGED_DECODE, "tcgen05": PAGED_TCGEN05}
 CACHE_F32, CACHE_BF16, CACHE_E4M3, CACHE_INT8 = 0, 1, 2, 3
 
 

@@ -374,9 +374,12 @@ int sdpa_cache_read(const sdpa_cache_t* cache, const sdpa_batch_t* batch, void* 
 typedef enum {
   SDPA_PAGED_AUTO = 0,
   SDPA_PAGED_EXACT = 1,  /* CUDA cores, fp32 arithmetic; every type, layout and option */
-  SDPA_PAGED_DECODE = 2  /* few new rows (max_q * Hq / Hkv <= 32): mma.sync, the keys of the whole batch
+  SDPA_PAGED_DECODE = 2, /* few new rows (max_q * Hq / Hkv <= 32): mma.sync, the keys of the whole batch
                             divided evenly over the SMs; BF16 I/O, d 64 or 128, page_size a multiple of
                             16, 16-byte aligned rows of q and the cache */
+  SDPA_PAGED_TCGEN05 = 3 /* chunks: TMA + tcgen05/TMEM tiles of 128 (token, head) rows; BF16 I/O, d 64
+                            or 128, Hq / Hkv <= 128, page_size a multiple of 16, 16-byte aligned rows
+                            of q, out and the cache */
 } sdpa_paged_path_t;
 
 /*

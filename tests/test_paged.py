@@ -225,3 +225,42 @@ def test_decode_equals_itself_and_any_split(cdt):
     a = run_case("decode", cdt, BF16, 8, 2, 128, 16, [5000, 300], None)
     b = run_case("decode", cdt, BF16, 8, 2, 128, 16, [5000, 300], None)
     assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ chunks on the tensor cores
+CHUNKS = [([1], [1]), ([128], [128]), ([129, 300], [129, 1]), ([1000], [100]), ([257, 40, 0, 640], [200, 40, 0, 3]),
+          ([2000], [17]), ([513], [513])]
+
+
+@pytest.mark.parametrize("kv,n", CHUNKS, ids=str)
+@pytest.mark.parametrize("cdt", [BF16, E4M3, INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunk_lengths(d, cdt, kv, n):
+    run_case("tcgen05", cdt, BF16, 8, 2, d, 32, kv, n, seed=len(kv))
+
+
+@pytest.mark.parametrize("Hq,Hkv,page,layout", [(2, 2, 16, "hnd"), (3, 1, 48, "nhd"), (12, 4, 256, "hnd"), (7, 1, 128, "hnd"),
+                                                (8, 1, 64, "nhd"), (40, 1, 80, "hnd"), (100, 1, 16, "hnd"), (128, 1, 32, "hnd")])
+@pytest.mark.parametrize("cdt", [BF16, E4M3, INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunk_heads_and_pages(d, cdt, Hq, Hkv, page, layout):
+    run_case("tcgen05", cdt, BF16, Hq, Hkv, d, page, [300, 77], [150, 30], layout=layout, seed=Hq)
+
+
+@pytest.mark.parametrize("kw", OPTIONS, ids=str)
+@pytest.mark.parametrize("cdt", [BF16, E4M3, INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunk_options(d, cdt, kw):
+    run_case("tcgen05", cdt, BF16, 8, 4, d, 16, [1000, 131, 400], [200, 131, 30], seed=d, **kw)
+
+
+@pytest.mark.parametrize("cdt", [BF16, E4M3])
+def test_chunk_more_rows_than_tokens(cdt):
+    run_case("tcgen05", cdt, BF16, 4, 2, 64, 16, [3, 0, 200], [150, 20, 220])
+
+
+@pytest.mark.parametrize("cdt", [BF16, E4M3, INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_auto_mixed(d, cdt):
+    """Single tokens, drafts and chunks of one batch: two kernels share it."""
+    run_case("auto", cdt, BF16, 8, 2, d, 16, [700, 65, 0, 300, 128, 1000], [1, 5, 0, 120, 128, 9], seed=7)
