@@ -12,6 +12,8 @@
 // held by a group of neighbouring lanes, 16 bytes of the wider side each, so
 // its amax is a few shuffles and nothing is staged; a warp keeps several rows
 // in flight to cover the latency of their loads.
+#include <algorithm>
+
 #include "paged.cuh"
 #include "pdl_launch.cuh"
 
@@ -64,92 +66,116 @@ struct WriteArgs {
   const void* v;
   long long kt, kh, vt, vh;
   int vec;  // sources and cache rows allow whole-piece accesses
-  FastDiv fd_h, fd_2h;
+  int tb;   // tokens of a block
+  int ppt;  // 16-byte pieces of a token: 2 Hkv D / E
+  FastDiv fd_ppt;
   int* err;
 };
 
-// T: elements given, C: elements kept.  Rows are numbered (token, k or v, head).
+constexpr int kMaxTok = 8;  // tokens of a block at most
+constexpr int kAhead = 4;   // pieces a thread has in flight
+
+// T: elements given, C: elements kept.  A block takes tb tokens, all heads of k
+// and v; a thread 16 bytes of a row at a time.  While its first pieces are on
+// their way one warp looks up where the tokens go.
 template <typename T, typename C, int D>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ WriteArgs a) {
-  constexpr int E = 16 / sizeof(T);  // elements a lane holds of a row
-  constexpr int G = D / E;           // lanes of a row
-  constexpr int RW = 32 / G;         // rows of a warp side by side
+  constexpr int E = 16 / sizeof(T);  // elements of a piece
+  constexpr int G = D / E;           // pieces (neighbouring lanes) of a row
+  __shared__ int s_page[kMaxTok], s_off[kMaxTok];
   sm100::grid_dep_launch();
   sm100::grid_dep_wait();
-  const int lane = threadIdx.x & 31;
-  const long long warp = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long rows = (long long)a.s.total_q * 2 * a.c.Hkv;
-  const long long r0 = warp * (RW * kRowsAhead);
-  if (r0 >= rows) return;
-  const int t0 = (int)fdiv((uint32_t)r0, a.fd_2h);
-  const int b0 = a.s.cu_q ? find_seq(a.s.cu_q, a.s.B, t0, lane) : t0;
-
-  float x[kRowsAhead][E];
-  long long dst[kRowsAhead], sdst[kRowsAhead];
-  bool live[kRowsAhead], is_v[kRowsAhead];
-  const int e0 = (lane % G) * E;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int t0 = blockIdx.x * a.tb;
+  const int pieces = min(a.tb, a.s.total_q - t0) * a.ppt;
+  for (int base = 0; base < pieces; base += kThreads * kAhead) {
+    float x[kAhead][E];
+    int tok[kAhead], row[kAhead];  // token of the block; row of the token: k heads, then v heads
 #pragma unroll
-  for (int u = 0; u < kRowsAhead; ++u) {
-    const long long r = r0 + u * RW + lane / G;
-    live[u] = r < rows;
-    const int rr = (int)(live[u] ? r : r0);
-    const int t = (int)fdiv((uint32_t)rr, a.fd_2h);
-    const int kvh = rr - t * 2 * a.c.Hkv;
-    is_v[u] = kvh >= a.c.Hkv;
-    const int h = is_v[u] ? kvh - a.c.Hkv : kvh;
-    const T* src = static_cast<const T*>(is_v[u] ? a.v : a.k) + (is_v[u] ? t * a.vt + h * a.vh : t * a.kt + h * a.kh);
-    if (a.vec) {
-      const uint4 raw = *reinterpret_cast<const uint4*>(src + e0);
-      const T* e = reinterpret_cast<const T*>(&raw);
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = base + u * kThreads + tid;
+      tok[u] = -1;
+      if (i < pieces) {
+        tok[u] = (int)fdiv((uint32_t)i, a.fd_ppt);
+        row[u] = (i - tok[u] * a.ppt) / G;
+        const bool is_v = row[u] >= a.c.Hkv;
+        const int h = is_v ? row[u] - a.c.Hkv : row[u];
+        const long long t = t0 + tok[u];
+        const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (is_v ? t * a.vt + h * a.vh : t * a.kt + h * a.kh) +
+                       (tid % G) * E;
+        if (a.vec) {
+          const uint4 raw = __ldg(reinterpret_cast<const uint4*>(src));
+          const T* e = reinterpret_cast<const T*>(&raw);
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[u][i] = to_f32(e[i]);
-    } else {
+          for (int n = 0; n < E; ++n) x[u][n] = to_f32(e[n]);
+        } else {
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[u][i] = to_f32(src[e0 + i]);
+          for (int n = 0; n < E; ++n) x[u][n] = to_f32(src[n]);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < E; ++n) x[u][n] = 0.f;
+      }
     }
-    // where the row goes: its position in its sequence, through the table
-    int b = b0, pos = -1;
-    if (a.s.cu_q) {
-      while (b + 1 < a.s.B && __ldg(a.s.cu_q + b + 1) <= t) ++b;
-    } else {
-      b = t;
+    if (base == 0) {
+      if (tid < 32) {
+        const int first = a.s.cu_q ? find_seq(a.s.cu_q, a.s.B, t0, lane) : 0;
+        if (lane < a.tb && t0 + lane < a.s.total_q) {
+          const int t = t0 + lane;
+          int b = t, page = -1, off = 0;
+          if (a.s.cu_q)
+            for (b = first; b + 1 < a.s.B && __ldg(a.s.cu_q + b + 1) <= t;) ++b;
+          const Seq q = seq_of(a.s, a.c, b, a.err);
+          // rows behind the last sequence and rows without a place are left out
+          if (t >= q.q0 && t < q.q0 + q.n) {
+            const int pos = q.L - q.n + (t - q.q0);
+            if (pos < 0) {
+              index_error(a.err);
+            } else {
+              page = page_or_bad(a.s, a.c, b, pos, a.err);
+              off = pos - (int)fdiv((uint32_t)pos, a.c.fd_page) * a.c.page_size;
+            }
+          }
+          s_page[lane] = page;
+          s_off[lane] = off;
+        }
+      }
+      __syncthreads();
     }
-    const Seq q = seq_of(a.s, a.c, b, a.err);
-    if (t >= q.q0 && t < q.q0 + q.n) {
-      pos = q.L - q.n + (t - q.q0);
-      if (pos < 0) index_error(a.err);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      float s = 1.f;
+      if (is_code<C>::value) {
+        float m = 0.f;
+#pragma unroll
+        for (int n = 0; n < E; ++n) m = fmaxf(m, fabsf(x[u][n]));
+#pragma unroll
+        for (int o = 1; o < G; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        s = fmaxf(__fdiv_rn(m, code_max<C>()), kScaleFloor);
+      }
+      const long long page = tok[u] >= 0 ? s_page[tok[u]] : -1;
+      if (page < 0) continue;
+      const int off = s_off[tok[u]];
+      const bool is_v = row[u] >= a.c.Hkv;
+      const int h = is_v ? row[u] - a.c.Hkv : row[u];
+      C* out = static_cast<C*>(is_v ? a.c.v : a.c.k) + (tid % G) * E +
+               (is_v ? page * a.c.vp + h * a.c.vh + off * a.c.vt : page * a.c.kp + h * a.c.kh + off * a.c.kt);
+      alignas(16) C y[E];
+#pragma unroll
+      for (int n = 0; n < E; ++n) y[n] = encode<T, C>(x[u][n], s);
+      if (a.vec) {
+        if constexpr (E * sizeof(C) == 16) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(y);
+        else if constexpr (E * sizeof(C) == 8) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
+        else *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<const uint32_t*>(y);
+      } else {
+#pragma unroll
+        for (int n = 0; n < E; ++n) out[n] = y[n];
+      }
+      if (is_code<C>::value && tid % G == 0) {
+        if (is_v) a.c.vs[page * a.c.vsp + h * a.c.vsh + off * a.c.vst] = s;
+        else a.c.ks[page * a.c.ksp + h * a.c.ksh + off * a.c.kst] = s;
+      }
     }
-    const int page = pos >= 0 ? page_or_bad(a.s, a.c, b, pos, a.err) : -1;
-    live[u] = live[u] && page >= 0;  // rows behind the last sequence and rows without a place are left out
-    const int off = pos - (int)fdiv((uint32_t)max(pos, 0), a.c.fd_page) * a.c.page_size;
-    dst[u] = is_v[u] ? page * a.c.vp + h * a.c.vh + off * a.c.vt : page * a.c.kp + h * a.c.kh + off * a.c.kt;
-    sdst[u] = is_v[u] ? page * a.c.vsp + h * a.c.vsh + off * a.c.vst : page * a.c.ksp + h * a.c.ksh + off * a.c.kst;
-  }
-#pragma unroll
-  for (int u = 0; u < kRowsAhead; ++u) {
-    float s = 1.f;
-    if (is_code<C>::value) {
-      float m = 0.f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) m = fmaxf(m, fabsf(x[u][i]));
-#pragma unroll
-      for (int o = 1; o < G; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      s = fmaxf(__fdiv_rn(m, code_max<C>()), kScaleFloor);
-    }
-    if (!live[u]) continue;
-    C* out = static_cast<C*>(is_v[u] ? a.c.v : a.c.k) + dst[u] + e0;
-    alignas(16) C y[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) y[i] = encode<T, C>(x[u][i], s);
-    if (a.vec) {
-      if constexpr (E * sizeof(C) == 16) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(y);
-      else if constexpr (E * sizeof(C) == 8) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
-      else *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<const uint32_t*>(y);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) out[i] = y[i];
-    }
-    if (is_code<C>::value && e0 == 0) (is_v[u] ? a.c.vs : a.c.ks)[sdst[u]] = s;
   }
 }
 
@@ -165,12 +191,28 @@ struct ReadArgs {
   int* err;
 };
 
+template <int N>
+struct alignas(N) Bytes {
+  uint8_t b[N];
+};
+// 32 bytes at once: one store per lane where the row's codes were one load
+__device__ __forceinline__ void store32(void* p, const void* src) {
+  const uint32_t* s = static_cast<const uint32_t*>(src);
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(s[0]), "r"(s[1]), "r"(s[2]),
+               "r"(s[3]), "r"(s[4]), "r"(s[5]), "r"(s[6]), "r"(s[7])
+               : "memory");
+}
+
 // C: elements kept, T: elements given out.  A block takes a run of tokens of
 // one (sequence, k or v, head): rows that follow each other in a page and in
-// the output.
+// the output.  A lane has 16 bytes of T of a row, 32 from 8-bit codes to bf16.
+template <typename C, typename T>
+constexpr int read_elems() {
+  return sizeof(C) == 1 && sizeof(T) == 2 ? 16 : 16 / sizeof(T);
+}
 template <typename C, typename T, int D>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadArgs a) {
-  constexpr int E = 16 / sizeof(T);
+  constexpr int E = read_elems<C, T>();
   constexpr int G = D / E;
   constexpr int RB = kThreads / G;  // rows of a block side by side
   sm100::grid_dep_launch();
@@ -185,13 +227,13 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   const int t0 = chunk * (RB * kRowsAhead);
   if (t0 >= L) return;
   const int e0 = (threadIdx.x % G) * E;
-  const C* src = static_cast<const C*>(is_v ? a.c.v : a.c.k) + h * (is_v ? a.c.vh : a.c.kh);
+  const C* src = static_cast<const C*>(is_v ? a.c.v : a.c.k) + h * (is_v ? a.c.vh : a.c.kh) + e0;
   const float* sc = is_v ? a.c.vs : a.c.ks;
   if (is_code<C>::value) sc += h * (is_v ? a.c.vsh : a.c.ksh);
   const long long sp = is_v ? a.c.vp : a.c.kp, stk = is_v ? a.c.vt : a.c.kt;
   const long long ssp = is_v ? a.c.vsp : a.c.ksp, sst = is_v ? a.c.vst : a.c.kst;
   const sdpa_strides_t os = is_v ? a.vs : a.ks;
-  T* dst = static_cast<T*>(is_v ? a.v : a.k) + (long long)b * os.b + (long long)h * os.h;
+  T* dst = static_cast<T*>(is_v ? a.v : a.k) + (long long)b * os.b + (long long)h * os.h + e0;
   int page[kRowsAhead];
 #pragma unroll
   for (int u = 0; u < kRowsAhead; ++u) {
@@ -205,11 +247,11 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
     const int t = t0 + u * RB + threadIdx.x / G;
     if (t < L) {
       const int off = t - (int)fdiv((uint32_t)t, a.c.fd_page) * a.c.page_size;
-      const C* row = src + page[u] * sp + off * stk + e0;
+      const C* row = src + page[u] * sp + off * stk;
       if (a.vec) {
-        if constexpr (E * sizeof(C) == 16) *reinterpret_cast<uint4*>(raw[u]) = *reinterpret_cast<const uint4*>(row);
-        else if constexpr (E * sizeof(C) == 8) *reinterpret_cast<uint2*>(raw[u]) = *reinterpret_cast<const uint2*>(row);
-        else *reinterpret_cast<uint32_t*>(raw[u]) = *reinterpret_cast<const uint32_t*>(row);
+        using V = Bytes<E * sizeof(C)>;
+        if constexpr (E * sizeof(C) == 16) *reinterpret_cast<uint4*>(raw[u]) = __ldg(reinterpret_cast<const uint4*>(row));
+        else *reinterpret_cast<V*>(raw[u]) = *reinterpret_cast<const V*>(row);
       } else {
 #pragma unroll
         for (int i = 0; i < E; ++i) raw[u][i] = row[i];
@@ -221,15 +263,16 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   for (int u = 0; u < kRowsAhead; ++u) {
     const int t = t0 + u * RB + threadIdx.x / G;
     if (t < L) {
-      alignas(16) T y[E];
+      alignas(32) T y[E];
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const float f = cache_elem(raw[u][i]);
         y[i] = from_f32<T>(is_code<C>::value ? f * s[u] : f);
       }
-      T* o = dst + (long long)t * os.t + e0;
+      T* o = dst + (long long)t * os.t;
       if (a.vec) {
-        *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(y);
+        if constexpr (E * sizeof(T) == 32) store32(o, y);
+        else *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(y);
       } else {
 #pragma unroll
         for (int i = 0; i < E; ++i) o[i] = y[i];
@@ -245,14 +288,18 @@ bool mult(const void* p, long long a, long long b, long long c, int esz, int n) 
 
 template <typename T, typename C, int D>
 cudaError_t write_one(WriteArgs& a, cudaStream_t stream) {
-  constexpr int E = 16 / sizeof(T), RW = 32 / (D / E);
+  constexpr int E = 16 / sizeof(T);
   const int nb = E * sizeof(C);
   a.vec = mult(a.k, a.kt, a.kh, 0, sizeof(T), 16) && mult(a.v, a.vt, a.vh, 0, sizeof(T), 16) &&
           mult(a.c.k, a.c.kp, a.c.kh, a.c.kt, sizeof(C), nb) && mult(a.c.v, a.c.vp, a.c.vh, a.c.vt, sizeof(C), nb);
-  const long long rows = (long long)a.s.total_q * 2 * a.c.Hkv;
-  const long long per = (long long)(kThreads / 32) * RW * kRowsAhead;
-  return launch_serialized(cache_write_kernel<T, C, D>, dim3((unsigned)((rows + per - 1) / per)), dim3(kThreads), 0,
-                           stream, a);
+  a.ppt = 2 * a.c.Hkv * (D / E);
+  a.fd_ppt = make_fastdiv((uint32_t)a.ppt);
+  // a token per block while that does not fill the SMs, more tokens to share
+  // the lookups and deepen the loads beyond that
+  const int fill = 8 * num_sms();
+  a.tb = std::max(1, std::min(kMaxTok, a.s.total_q / fill));
+  return launch_serialized(cache_write_kernel<T, C, D>, dim3((unsigned)((a.s.total_q + a.tb - 1) / a.tb)),
+                           dim3(kThreads), 0, stream, a);
 }
 template <typename T, typename C>
 cudaError_t write_d(WriteArgs& a, cudaStream_t stream) {
@@ -266,9 +313,9 @@ cudaError_t write_d(WriteArgs& a, cudaStream_t stream) {
 
 template <typename C, typename T, int D>
 cudaError_t read_one(ReadArgs& a, cudaStream_t stream) {
-  constexpr int E = 16 / sizeof(T), RB = kThreads / (D / E);
-  const int nb = E * sizeof(C);
-  a.vec = mult(a.k, a.ks.b, a.ks.h, a.ks.t, sizeof(T), 16) && mult(a.v, a.vs.b, a.vs.h, a.vs.t, sizeof(T), 16) &&
+  constexpr int E = read_elems<C, T>(), RB = kThreads / (D / E);
+  const int nb = E * sizeof(C), no = E * sizeof(T);
+  a.vec = mult(a.k, a.ks.b, a.ks.h, a.ks.t, sizeof(T), no) && mult(a.v, a.vs.b, a.vs.h, a.vs.t, sizeof(T), no) &&
           mult(a.c.k, a.c.kp, a.c.kh, a.c.kt, sizeof(C), nb) && mult(a.c.v, a.c.vp, a.c.vh, a.c.vt, sizeof(C), nb);
   a.chunks = (a.T + RB * kRowsAhead - 1) / (RB * kRowsAhead);
   a.fd_chunks = make_fastdiv((uint32_t)a.chunks);
@@ -293,8 +340,6 @@ cudaError_t launch_cache_write(const CacheView& c, const BatchView& s, const voi
                                cudaStream_t stream) {
   WriteArgs a;
   a.c = c; a.s = s; a.k = k; a.v = v; a.kt = kt; a.kh = kh; a.vt = vt; a.vh = vh; a.err = err;
-  a.fd_h = make_fastdiv((uint32_t)c.Hkv);
-  a.fd_2h = make_fastdiv((uint32_t)(2 * c.Hkv));
   const bool f = dtype == SDPA_F32;
   switch (c.dtype) {
     case SDPA_CACHE_F32: return write_d<float, float>(a, stream);

@@ -125,6 +125,13 @@ __device__ __forceinline__ uint32_t biased_bytes_to_half2(uint32_t x, uint32_t s
   return o;
 }
 
+// 1 / x to within one rounding step (2^-23 relative); x = inf gives 0.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // One element of a cache row as fp32.
 __device__ __forceinline__ float cache_elem(float x) { return x; }
 __device__ __forceinline__ float cache_elem(__nv_bfloat16 x) { return __bfloat162float(x); }

@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
         float lg;
         asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(vs));
         sc[2 * KS + lane] = lg;
-        sc[3 * KS + lane] = __frcp_rn(vs);
+        sc[3 * KS + lane] = rcp_approx(vs);
       }
       issue(step + NST - 1);
       lookup(step + NST);
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
               if constexpr (MOD) {
                 float y = s[m][n][k] * xscale[m][e] * ks2[k & 1];
                 if (p.softcap > 0.f)  // c tanh(y / c) = c - 2 c / (1 + e^(2 y / c))
-                  y = fmaf(-2.f * p.softcap, __frcp_rn(1.f + ex2_approx(y * icap2)), p.softcap);
+                  y = fmaf(-2.f * p.softcap, rcp_approx(1.f + ex2_approx(y * icap2)), p.softcap);
                 y = fmaf(slope[m][e], (float)(j - pos[m][e]), y);
                 x = fmaf(y, kLog2e, lv2[k & 1]);
               } else if constexpr (F16) {
@@ -811,12 +811,9 @@ cudaError_t decode_rows(DecodeArgs& a, bool mod, int ctas, cudaStream_t stream) 
 // can have more, else 32.
 int row_limit(const PagedParams& p) { return (long long)p.s.max_q * p.group <= 16 ? 16 : kDecodeRows; }
 
-// One CTA per unit and no merge launch where the caches are so short that the
-// longest unit is no more than two tiles of 64 or 128 keys.
-bool whole_units(const PagedParams& p) {
-  const int tile = p.c.dtype == SDPA_CACHE_BF16 && p.c.d == 128 ? 64 : 128;
-  return (long long)p.s.max_pages * p.c.page_size <= 2 * tile;
-}
+// One CTA per unit and no merge launch where the caches are so short that
+// splitting them would cost more than it gives.  TODO-FIGURES
+bool whole_units(const PagedParams& p) { return (long long)p.s.max_pages * p.c.page_size <= 512; }
 
 // One resident wave.
 int decode_ctas(const PagedParams& p) {

@@ -445,18 +445,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       const int ct = tid - 320;  // 0 .. 63
       bool ok = true;
       int r_next = 0;
-      // scales of this thread's two keys of a tile, fetched a tile ahead
+      // scales of this thread's two keys of a tile: page numbers fetched two
+      // tiles ahead, scales one, so neither load is waited for
       float ks_n[2], vs_n[2];
-      auto fetch = [&](int jj) {
+      int pg_n[2];
+      auto seen_key = [&](int jj, int x) {
+        const int key = (j_begin + jj) * BN + x * kHalf + ct;
+        return jj < n_tiles && key >= klo && key < khi ? key : -1;
+      };
+      auto fetch_pages = [&](int jj) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int key = (j_begin + jj) * BN + x * kHalf + ct;
+          const int key = seen_key(jj, x);
+          pg_n[x] = key >= 0 ? page_of(p.s, p.c, u.b, key, p.err) : 0;
+        }
+      };
+      auto fetch_scales = [&](int jj) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int key = seen_key(jj, x);
           ks_n[x] = vs_n[x] = 1.f;
-          if (jj < n_tiles && key >= klo && key < khi) {
-            const long long pg = page_of(p.s, p.c, u.b, key, p.err);
+          if (key >= 0) {
+            const long long pg = pg_n[x];
             const int off = key - (int)fdiv((uint32_t)key, p.c.fd_page) * p.c.page_size;
-            ks_n[x] = p.c.ks[pg * p.c.ksp + u.hk * p.c.ksh + off * p.c.kst];
-            vs_n[x] = p.c.vs[pg * p.c.vsp + u.hk * p.c.vsh + off * p.c.vst];
+            ks_n[x] = __ldg(p.c.ks + pg * p.c.ksp + u.hk * p.c.ksh + off * p.c.kst);
+            vs_n[x] = __ldg(p.c.vs + pg * p.c.vsp + u.hk * p.c.vsh + off * p.c.vst);
           }
         }
       };
@@ -471,33 +484,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           constexpr int kPieces = D / 16;  // 16 codes each
           constexpr int kPass = kConv / kPieces;
           const int pc = ct % kPieces, r0 = ct / kPieces;
-          const uint8_t* src = sRaw + rs * L::kRaw;
+          const uint8_t* src = sRaw + rs * L::kRaw + r0 * D + pc * 16;
+          const int key0 = (j_begin + jj) * BN + x * kHalf + r0;
+          const bool all = key0 - r0 >= klo && key0 - r0 + kHalf <= khi;
+          // codes 16 pc ..: panel pc / 4, 16-byte chunks 2 (pc % 4) and the next, at chunk ^ (row % 8)
+          uint8_t* line = dst + (pc >> 2) * BN * 128 + (x * kHalf + r0) * 128;
+          const int c0 = 2 * (pc & 3), sw = r0 & 7;
+          static_assert(kPass % 8 == 0, "a thread's rows have one swizzle");
+          constexpr int kBatch = 4;  // pieces loaded together
 #pragma unroll
-          for (int i = 0; i < kHalf / kPass; ++i) {
-            const int r = i * kPass + r0, row = x * kHalf + r;
-            const int key = (j_begin + jj) * BN + row;
-            uint4 w = *reinterpret_cast<const uint4*>(src + r * D + pc * 16);
-            if (key < klo || key >= khi) w = make_uint4(0, 0, 0, 0);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-            uint32_t h[8];
+          for (int i0 = 0; i0 < kHalf / kPass; i0 += kBatch) {
+            uint4 w[kBatch];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if constexpr (KV == KV_E4M3) {
-                e4m3x4_to_half2(ws[q], h[2 * q], h[2 * q + 1]);
-              } else {
-                const uint32_t y = ws[q] ^ 0x80808080u;
-                h[2 * q] = biased_bytes_to_half2(y, 0x4140);
-                h[2 * q + 1] = biased_bytes_to_half2(y, 0x4342);
-              }
+            for (int i = 0; i < kBatch; ++i) {
+              w[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * kPass * D);
+              const int key = key0 + (i0 + i) * kPass;
+              if (!all && (key < klo || key >= khi)) w[i] = make_uint4(0, 0, 0, 0);
             }
-            // codes 16 pc ..: panel pc / 4, 16-byte chunks 2 (pc % 4) and the next, at chunk ^ (row % 8);
-            // the upper panel's lanes store the second first, so 8 lanes hit 8 chunks
-            uint8_t* line = dst + (pc >> 2) * BN * 128 + row * 128;
-            const bool up = pc >= 4;
-            const int c0 = 2 * (pc & 3) + (up ? 1 : 0), c1 = c0 ^ 1;
-            const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-            *reinterpret_cast<uint4*>(line + ((c0 ^ (row & 7)) << 4)) = up ? b : a;
-            *reinterpret_cast<uint4*>(line + ((c1 ^ (row & 7)) << 4)) = up ? a : b;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int row = (i0 + i) * kPass;  // past r0
+              const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+              uint32_t h[8];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if constexpr (KV == KV_E4M3) {
+                  e4m3x4_to_half2(ws[q], h[2 * q], h[2 * q + 1]);
+                } else {
+                  const uint32_t y = ws[q] ^ 0x80808080u;
+                  h[2 * q] = biased_bytes_to_half2(y, 0x4140);
+                  h[2 * q + 1] = biased_bytes_to_half2(y, 0x4342);
+                }
+              }
+              *reinterpret_cast<uint4*>(line + row * 128 + ((c0 ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(line + row * 128 + (((c0 + 1) ^ sw) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
           }
           mbar_arrive(&raw_empty[rs]);
           ++r_next;
@@ -506,7 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         fence_proxy_async_shared();
         mbar_arrive(is_v ? &v_full[s] : &k_full[s]);
       };
-      fetch(0);
+      fetch_pages(0);
+      fetch_scales(0);
+      fetch_pages(1);
       for (int jj = 0; jj <= n_tiles && ok; ++jj) {
         if (jj < n_tiles) {
           float* sc = sSc + (jj % SR) * 3 * BN;
@@ -523,10 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(vs_n[x]));
             sc[x * kHalf + ct] = ks_n[x];
             sc[BN + x * kHalf + ct] = lg;
-            sc[2 * BN + x * kHalf + ct] = __frcp_rn(vs_n[x]);
+            sc[2 * BN + x * kHalf + ct] = rcp_approx(vs_n[x]);
           }
           mbar_arrive(&sc_full[jj % SR]);
-          fetch(jj + 1);
+          fetch_scales(jj + 1);
+          fetch_pages(jj + 2);
           convert(false, jj);
         }
         if (ok && jj > 0) convert(true, jj - 1);
@@ -632,8 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           for (int c = 0; c < BN / 2; ++c) {
             float lo, hi;
             f2_split(x2[c], lo, hi);
-            lo = fmaf(-2.f * cap_out, __frcp_rn(1.f + ex2_approx(lo * cap_in)), cap_out);
-            hi = fmaf(-2.f * cap_out, __frcp_rn(1.f + ex2_approx(hi * cap_in)), cap_out);
+            lo = fmaf(-2.f * cap_out, rcp_approx(1.f + ex2_approx(lo * cap_in)), cap_out);
+            hi = fmaf(-2.f * cap_out, rcp_approx(1.f + ex2_approx(hi * cap_in)), cap_out);
             x2[c] = f2(lo, hi);
           }
         }

@@ -163,13 +163,13 @@ def _strides(t) -> sdpa_strides_t:
 
 def _batch(cache: KVCache, page_table, kv_lens, cu_q, total_q: int, max_q: Optional[int]) -> sdpa_batch_t:
     import torch
-    dev = cache.device
+    dev, i32 = cache.device, torch.int32
     for t, dim, name in ((page_table, 2, "page_table"), (kv_lens, 1, "kv_lens"), (cu_q, 1, "cu_q")):
         if t is None and name == "cu_q":
             continue
-        if t.dtype != torch.int32 or t.dim() != dim or t.device != dev:
+        if t.dtype != i32 or t.dim() != dim or t.device != dev:
             raise ValueError(f"{name} must be a {dim}-D int32 tensor on the cache's device")
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
+        if not t.is_contiguous() and t.shape[-1] > 1 and t.stride(-1) != 1:
             raise ValueError(f"{name} must have a contiguous last axis")
     B, width = kv_lens.shape[0], page_table.shape[1]
     if page_table.shape[0] != B or (cu_q is not None and cu_q.shape[0] != B + 1):
@@ -207,11 +207,12 @@ def _switch(device, stream):
 
 
 class _Here:
-    """The current stream of the current device."""
+    """The current stream of the current device, by its handle: asking for the
+    Stream object costs more than the rest of a call's checks."""
 
     def __enter__(self):
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
     def __exit__(self, *exc):
         return False
