@@ -88,14 +88,18 @@ __device__ __forceinline__ Seq seq_of(const BatchView& s, const CacheView& c, in
   return r;
 }
 
-// Page of token t of sequence b; a bad entry reads as -1.
+// Page of token t of sequence b as the table has it; a bad one becomes -1 in
+// good_page.  (Apart, so that a load may be on its way long before its use.)
+__device__ __forceinline__ int page_entry(const BatchView& s, const CacheView& c, int b, int t) {
+  return __ldg(s.table + (long long)b * s.table_stride + fdiv((uint32_t)t, c.fd_page));
+}
+__device__ __forceinline__ int good_page(const CacheView& c, int p, int* err) {
+  if ((unsigned)p < (unsigned)c.num_pages) return p;
+  index_error(err);
+  return -1;
+}
 __device__ __forceinline__ int page_or_bad(const BatchView& s, const CacheView& c, int b, int t, int* err) {
-  const int p = __ldg(s.table + (long long)b * s.table_stride + fdiv((uint32_t)t, c.fd_page));
-  if ((unsigned)p >= (unsigned)c.num_pages) {
-    index_error(err);
-    return -1;
-  }
-  return p;
+  return good_page(c, page_entry(s, c, b, t), err);
 }
 __device__ __forceinline__ int page_of(const BatchView& s, const CacheView& c, int b, int t, int* err) {
   return max(0, page_or_bad(s, c, b, t, err));

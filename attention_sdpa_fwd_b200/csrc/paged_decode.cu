@@ -292,13 +292,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
     auto fetch = [&](int span) {
       const int step = span * kSpan + lane / kGroups;
       const int t = base + step * C::kKeys + 16 * (lane % kGroups);
-      return step < ntile && t < khi && t + 16 > klo ? page_of(p.s, p.c, b, t, p.err) : 0;
+      return step < ntile && t < khi && t + 16 > klo ? page_entry(p.s, p.c, b, t) : 0;
     };
     int pages = fetch(0), pages_next = fetch(1);
+    pages = max(0, good_page(p.c, pages, p.err));
     // where this lane's first row of each 16 tokens of a step is
     auto lookup = [&](int step) {
       if (step > 0 && step % kSpan == 0) {
-        pages = pages_next;
+        pages = max(0, good_page(p.c, pages_next, p.err));
         pages_next = fetch(step / kSpan + 1);
       }
       const int t0 = base + step * C::kKeys;

@@ -6,23 +6,29 @@
 // tile is token r / G, query head r % G of the G heads that share the kv head,
 // so a tile is full whatever G is, K and V are read once for all G heads, and
 // the causal diagonal costs 128 / G tokens.  Q comes as one TMA box
-// (64 columns, G heads, 128 / G tokens) per panel.  Roles, 384 threads:
+// (64 columns, G heads, 128 / G tokens) per panel.  Roles, 384 threads, 512 for codes:
 //   warps 0-3, 4-7  softmax of tile A, B (thread = row = TMEM lane)
 //   warp  8         producer: K / V pages by TMA, one box per run of tokens
 //                   inside a page, page numbers a tile ahead
 //   warp  9         TMEM owner, MMA issuer
-//   warps 10-11     codes: the converters
+//   warps 12-15     codes: the converters (10 and 11 idle)
 // The tile pipeline (S_t = Q_t.K^T, softmax, O_t += P_t.V, stale-max rescale)
 // is that of the dense kernel, flash_tc.cu: at head_dim 128 P_t overwrites S_t,
 // at 64 it has its own columns and S_t runs a tile ahead.
 //
-// 8-bit caches: raw pages land in a ring of 64-key pieces; the converters turn
-// codes into f16 (exactly) in the K / V stages, in the 128-byte swizzle the
-// MMA reads, and put ks, log2 vs and 1 / vs of the tile's keys beside them.
-// The softmax warps scale their Q row in place by a power of two into f16 (its
-// largest element to [2^14, 2^15)).  Scores are acc * ks_j; V's scale goes into
-// the exponent, t_j = x_j log2e + log2 vs_j, p_j = 2^(t_j - m), and out is
-// sum p_j code_j / sum p_j (1 / vs_j), as in the decode kernel.
+// 8-bit caches: raw pages land in a ring of 64-key pieces, and four converter
+// warps, 32 keys of a tile each, turn codes into f16 in the K / V stages, in the
+// 128-byte swizzle the MMA reads.  Every row is multiplied by its scale on the
+// way, relative to a power of two 2^e of its 32 keys that puts their largest
+// scale in [64, 128): code * scale 2^-e is below 57344 and is rounded
+// once, to f16 (2^-11; the scale enters as a sum of two f16), eight times finer
+// than the bf16 the cache stands in for.  What the softmax warps see of it is a
+// factor 2^ek for 32 scores and, for V, an offset ev of 32 exponents:
+//     p_j = 2^(x_j log2e + ev - m),  out = sum p_j v_j 2^-ev / sum p_j 2^-ev
+// (Scales by column there, exact, cost three shared-memory vectors per row and
+// tile and twice the time.)  The softmax warps scale their Q row in place by a
+// power of two into f16, its largest element to [2^14, 2^15).  P is f16 as in
+// the decode kernel: at most 2^15, offset by 2^12.
 //
 // Units of one launch differ in length (causal), so later query blocks, the
 // longer ones, start first.  When there are fewer units than SMs every unit's
@@ -43,15 +49,15 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 384;
+// Codes take four more warps, the converters.
+template <int KV> constexpr int kThreadsOf = KV == 0 ? 384 : 512;
 constexpr int kRows = 128;           // of a tile
 constexpr int BN = 128;              // keys of a tile
 constexpr int kHalf = 64;            // keys of a raw piece
-constexpr int kConv = 64;            // converter threads
 constexpr int kMaxSplit = 16;
-constexpr int kRegsLaunch = 168;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+template <int KV> constexpr int kRegsLaunch = KV == 0 ? 168 : 128;  // registers a thread is launched with
 
 enum { KV_BF16 = 0, KV_E4M3 = 1, KV_INT8 = 2 };
 
@@ -72,8 +78,8 @@ template <int KV, int D>
 struct TcLayout {
   static constexpr bool kCodes = KV != KV_BF16;
   static constexpr int NS = D == 64 ? 3 : 2;
-  static constexpr int NR = D == 64 ? 4 : 3;        // raw pieces
-  static constexpr int SR = D == 64 ? 8 : 4;        // tiles of scales kept: see the softmax loop
+  static constexpr int NR = 4;                      // raw pieces; even: each converter has its own
+  static constexpr int SR = D == 64 ? 8 : 4;        // tiles whose exponents are kept: see the converters
   static constexpr int kPanels = D / 64;
   static constexpr int kQBytes = kPanels * kRows * 128;
   static constexpr int kKVBytes = kPanels * BN * 128;
@@ -82,8 +88,8 @@ struct TcLayout {
   static constexpr int oK = oQ + 2 * kQBytes;
   static constexpr int oV = oK + NS * kKVBytes;
   static constexpr int oRaw = oV + NS * kKVBytes;
-  static constexpr int oSc = oRaw + NR * kRaw;       // [SR][3][BN] floats
-  static constexpr int oBar = oSc + (kCodes ? SR * 3 * BN * 4 : 0);
+  static constexpr int oSc = oRaw + NR * kRaw;       // [SR][4] float4: 2^ek, ev, 2^-ev of 32 keys
+  static constexpr int oBar = oSc + (kCodes ? SR * 4 * 16 : 0);
   static constexpr int kBars = 4 * NS + 16 + 2 * NR + SR;
   static constexpr int kTotal = oBar + kBars * 8 + 64;
   static constexpr int kAlloc = kTotal + 1024;
@@ -107,6 +113,7 @@ __device__ __forceinline__ int blocks_of(const TcPagedArgs& a, int b) {
 
 // Unit `unit` of the launch, blocks numbered from the last one down; false past
 // the last.  The whole CTA takes part.
+template <int kThreads>
 __device__ __forceinline__ bool find_unit(const TcPagedArgs& a, int unit, TcUnit& u) {
   __shared__ int s_part[kThreads / 32], s_found[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -164,21 +171,22 @@ __device__ __forceinline__ bool find_unit(const TcPagedArgs& a, int unit, TcUnit
 }
 
 template <int KV, int D, bool MOD>
-__global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ TcPagedArgs args) {
+__global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __grid_constant__ TcPagedArgs args) {
   using L = TcLayout<KV, D>;
   constexpr bool kCodes = L::kCodes;
   constexpr bool kPSep = D == 64;
   constexpr int NS = L::NS, NR = L::NR, SR = L::SR;
   constexpr float kLag = kCodes ? 3.f : 8.f, kOffset = kCodes ? 12.f : 0.f;
-  constexpr int kRegsSoftmax = 216, kRegsOther = 72;
-  static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "register split");
+  // setmaxnreg: what the softmax warpgroups get the other one (codes: two) gave up
+  constexpr int kRegsSoftmax = kCodes ? 192 : 216, kRegsOther = kCodes ? 64 : 72;
+  static_assert(256 * kRegsSoftmax + (kThreadsOf<KV> - 256) * kRegsOther <= kThreadsOf<KV> * kRegsLaunch<KV>, "register split");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem + L::oQ;
   uint8_t* sK = smem + L::oK;
   uint8_t* sV = smem + L::oV;
   uint8_t* sRaw = smem + L::oRaw;
-  float* sSc = reinterpret_cast<float*>(smem + L::oSc);
+  float4* sSc = reinterpret_cast<float4*>(smem + L::oSc);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::oBar);
   uint64_t* k_full = bars;
   uint64_t* v_full = bars + NS;
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   const int unit = (int)fdiv(blockIdx.x, args.fd_split);
   const int sidx = blockIdx.x - unit * args.n_split;
   TcUnit u;
-  if (!find_unit(args, unit, u)) return;
+  if (!find_unit<kThreadsOf<KV>>(args, unit, u)) return;
   const int span = u.je - u.jb;
   const int j_begin = u.jb + (int)fdiv((uint32_t)(span * sidx), args.fd_split);
   const int n_tiles = u.jb + (int)fdiv((uint32_t)(span * (sidx + 1)), args.fd_split) - j_begin;
@@ -223,11 +231,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     mbar_init(q_ready, 2 * kRows);
     if (kCodes) {
       for (int i = 0; i < NS; ++i) {
-        mbar_init(&k_full[i], kConv);
-        mbar_init(&v_full[i], kConv);
+        mbar_init(&k_full[i], 4);
+        mbar_init(&v_full[i], 4);
       }
-      for (int i = 0; i < NR; ++i) mbar_init(&raw_empty[i], kConv);
-      for (int i = 0; i < SR; ++i) mbar_init(&sc_full[i], kConv);
+      for (int i = 0; i < NR; ++i) mbar_init(&raw_empty[i], 2);
+      for (int i = 0; i < SR; ++i) mbar_init(&sc_full[i], 4);
     }
     fence_mbar_init();
     if (n_tiles > 0) {
@@ -440,120 +448,142 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       }
       mma_commit_w(&o_done[0]);
       mma_commit_w(&o_done[1]);
-    } else if (kCodes && warp >= 10 && n_tiles > 0) {
+    } else if (kCodes && warp >= 12 && n_tiles > 0) {
       // ------------------------------------------------------------ converters
-      const int ct = tid - 320;  // 0 .. 63
+      // Warp 12 + i has keys 32 i .. of every tile, a key per lane.
+      const int part = warp - 12, half = part >> 1;
       bool ok = true;
-      int r_next = 0;
-      // scales of this thread's two keys of a tile: page numbers fetched two
-      // tiles ahead, scales one, so neither load is waited for
-      float ks_n[2], vs_n[2];
-      int pg_n[2];
-      auto seen_key = [&](int jj, int x) {
-        const int key = (j_begin + jj) * BN + x * kHalf + ct;
+      int r_next = half;  // raw pieces alternate between the halves
+      // The scales of this lane's key: its page number is fetched two tiles
+      // ahead, the scales one, so neither load is waited for.
+      float ks_n = 0.f, vs_n = 0.f;
+      int pg_n = 0;
+      auto seen_key = [&](int jj) {
+        const int key = (j_begin + jj) * BN + part * 32 + lane;
         return jj < n_tiles && key >= klo && key < khi ? key : -1;
       };
-      auto fetch_pages = [&](int jj) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int key = seen_key(jj, x);
-          pg_n[x] = key >= 0 ? page_of(p.s, p.c, u.b, key, p.err) : 0;
-        }
+      auto fetch_page = [&](int jj) {
+        const int key = seen_key(jj);
+        pg_n = key >= 0 ? page_entry(p.s, p.c, u.b, key) : 0;
       };
       auto fetch_scales = [&](int jj) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int key = seen_key(jj, x);
-          ks_n[x] = vs_n[x] = 1.f;
-          if (key >= 0) {
-            const long long pg = pg_n[x];
-            const int off = key - (int)fdiv((uint32_t)key, p.c.fd_page) * p.c.page_size;
-            ks_n[x] = __ldg(p.c.ks + pg * p.c.ksp + u.hk * p.c.ksh + off * p.c.kst);
-            vs_n[x] = __ldg(p.c.vs + pg * p.c.vsp + u.hk * p.c.vsh + off * p.c.vst);
-          }
+        const int key = seen_key(jj);
+        ks_n = vs_n = 0.f;  // rows nobody sees become zeros
+        if (key >= 0) {
+          const long long pg = max(0, good_page(p.c, pg_n, p.err));
+          const int off = key - (int)fdiv((uint32_t)key, p.c.fd_page) * p.c.page_size;
+          ks_n = __ldg(p.c.ks + pg * p.c.ksp + u.hk * p.c.ksh + off * p.c.kst);
+          vs_n = __ldg(p.c.vs + pg * p.c.vsp + u.hk * p.c.vsh + off * p.c.vst);
         }
       };
-      auto convert = [&](bool is_v, int jj) {
-        const int s = jj % NS, use = jj / NS;
-        if (use > 0) ok = wait_all(mbar_wait(is_v ? &v_empty[s] : &k_empty[s], (use - 1) & 1, abort_v, p.err));
-        uint8_t* dst = (is_v ? sV : sK) + s * L::kKVBytes;
-        for (int x = 0; x < 2 && ok; ++x) {
-          const int rs = r_next % NR;
-          ok = wait_all(mbar_wait(&raw_full[rs], (r_next / NR) & 1, abort_v, p.err));
-          if (!ok) break;
-          constexpr int kPieces = D / 16;  // 16 codes each
-          constexpr int kPass = kConv / kPieces;
-          const int pc = ct % kPieces, r0 = ct / kPieces;
-          const uint8_t* src = sRaw + rs * L::kRaw + r0 * D + pc * 16;
-          const int key0 = (j_begin + jj) * BN + x * kHalf + r0;
-          const bool all = key0 - r0 >= klo && key0 - r0 + kHalf <= khi;
-          // codes 16 pc ..: panel pc / 4, 16-byte chunks 2 (pc % 4) and the next, at chunk ^ (row % 8)
-          uint8_t* line = dst + (pc >> 2) * BN * 128 + (x * kHalf + r0) * 128;
-          const int c0 = 2 * (pc & 3), sw = r0 & 7;
-          static_assert(kPass % 8 == 0, "a thread's rows have one swizzle");
-          constexpr int kBatch = 4;  // pieces loaded together
-#pragma unroll
-          for (int i0 = 0; i0 < kHalf / kPass; i0 += kBatch) {
-            uint4 w[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              w[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * kPass * D);
-              const int key = key0 + (i0 + i) * kPass;
-              if (!all && (key < klo || key >= khi)) w[i] = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int row = (i0 + i) * kPass;  // past r0
-              const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-              uint32_t h[8];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if constexpr (KV == KV_E4M3) {
-                  e4m3x4_to_half2(ws[q], h[2 * q], h[2 * q + 1]);
-                } else {
-                  const uint32_t y = ws[q] ^ 0x80808080u;
-                  h[2 * q] = biased_bytes_to_half2(y, 0x4140);
-                  h[2 * q + 1] = biased_bytes_to_half2(y, 0x4342);
-                }
-              }
-              *reinterpret_cast<uint4*>(line + row * 128 + ((c0 ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4*>(line + row * 128 + (((c0 + 1) ^ sw) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-            }
-          }
-          mbar_arrive(&raw_empty[rs]);
-          ++r_next;
-        }
-        if (!ok) return;
-        fence_proxy_async_shared();
-        mbar_arrive(is_v ? &v_full[s] : &k_full[s]);
+      // The largest scale's exponent less 6, and scale 2^-e of a key as the sum
+      // of two f16 (the first in the low half).
+      auto common = [&](float s) {
+        const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(s));
+        return max(-36, (int)(top >> 23) - 127 - 6);
       };
-      fetch_pages(0);
+      auto two_halves = [](float s, int e) {
+        const float r = s * __uint_as_float((uint32_t)(127 - e) << 23);
+        const __half hi = __float2half_rn(r);
+        const __half lo = __float2half_rn(r - __half2float(hi));
+        return (uint32_t)__half_as_ushort(hi) | ((uint32_t)__half_as_ushort(lo) << 16);
+      };
+      constexpr int kPieces = D / 16;        // of a row, 16 codes each
+      constexpr int kPass = 32 / kPieces;    // rows of a pass
+      const int pc = lane % kPieces, r0 = lane / kPieces;
+      fetch_page(0);
       fetch_scales(0);
-      fetch_pages(1);
-      for (int jj = 0; jj <= n_tiles && ok; ++jj) {
-        if (jj < n_tiles) {
-          float* sc = sSc + (jj % SR) * 3 * BN;
+      fetch_page(1);
+      uint32_t v_prev = 0, v_now = 0;  // V's scales of the last two tiles
+      // K(0), then K(j + 1) and V(j) in turn, in one rolled loop: unrolled twice
+      // over, this code and the softmax warps' do not fit the instruction cache
+      // together (the converters then took 3400 cycles a tile, not TODO)
+#pragma unroll 1
+      for (int it = 0; it < 2 * n_tiles && ok; ++it) {
+        const bool is_v = it == 2 * n_tiles - 1 || (it > 0 && !(it & 1));
+        const int jj = is_v ? (it - 1) >> 1 : (it + 1) >> 1;
+        const int s = jj % NS, use = jj / NS;
+        uint32_t scales = v_prev;
+        if (use > 0) ok = wait_all(mbar_wait(is_v ? &v_empty[s] : &k_empty[s], (use - 1) & 1, abort_v, p.err));
+        if (!ok) break;
+        if (!is_v) {
+          const int ek = common(ks_n), ev = common(vs_n);
+          scales = two_halves(ks_n, ek);
+          v_prev = v_now;
+          v_now = two_halves(vs_n, ev);
           // The tile that used this slot, jj - SR, is behind every softmax
           // warp: K stage jj % NS being free means S(jj - NS) is complete, and
           // that S is only issued once tile jj - NS - 1's scores (head_dim 64)
           // or P (128) were taken from tensor memory: tiles up to jj - NS - 2
           // (64) or jj - NS - 1 (128) are finished, and SR >= NS + 2.
-          if (jj >= NS) ok = wait_all(mbar_wait(&k_empty[jj % NS], (jj / NS - 1) & 1, abort_v, p.err));
-          if (!ok) break;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float lg;
-            asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(vs_n[x]));
-            sc[x * kHalf + ct] = ks_n[x];
-            sc[BN + x * kHalf + ct] = lg;
-            sc[2 * BN + x * kHalf + ct] = rcp_approx(vs_n[x]);
+          if (lane == 0) {
+            sSc[(jj % SR) * 4 + part] = make_float4(__uint_as_float((uint32_t)(127 + ek) << 23), (float)ev,
+                                                    __uint_as_float((uint32_t)(127 - ev) << 23), 0.f);
+            mbar_arrive(&sc_full[jj % SR]);
           }
-          mbar_arrive(&sc_full[jj % SR]);
           fetch_scales(jj + 1);
-          fetch_pages(jj + 2);
-          convert(false, jj);
+          fetch_page(jj + 2);
+        } else if (jj == n_tiles - 1) {
+          scales = v_now;
         }
-        if (ok && jj > 0) convert(true, jj - 1);
+        const int rs = r_next % NR;
+        ok = wait_all(mbar_wait(&raw_full[rs], (r_next / NR) & 1, abort_v, p.err));
+        if (!ok) break;
+        const int key0 = (j_begin + jj) * BN + part * 32;
+        const bool all = key0 >= klo && key0 + 32 <= khi;
+        const uint8_t* src = sRaw + rs * L::kRaw + ((part & 1) * 32 + r0) * D + pc * 16;
+        // codes 16 pc ..: panel pc / 4, 16-byte chunks 2 (pc % 4) and the next, at chunk ^ (row % 8)
+        uint8_t* line = (is_v ? sV : sK) + s * L::kKVBytes + (pc >> 2) * BN * 128 + (part * 32 + r0) * 128;
+        const int c0 = 2 * (pc & 3);
+        constexpr int kBatch = 4;  // pieces loaded together
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += kBatch * kPass) {
+          uint4 w[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            w[i] = *reinterpret_cast<const uint4*>(src + (i0 + i * kPass) * D);
+            const int key = key0 + i0 + i * kPass + r0;
+            if (!all && (key < klo || key >= khi)) w[i] = make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int first = i0 + i * kPass;  // this warp's row first + r0
+            const uint32_t sc = __shfl_sync(0xffffffffu, scales, first + r0);
+            const uint32_t hi2 = __byte_perm(sc, 0, 0x1010), lo2 = __byte_perm(sc, 0, 0x3232);
+            __half2 shi, slo;
+            memcpy(&shi, &hi2, 4);
+            memcpy(&slo, &lo2, 4);
+            const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if constexpr (KV == KV_E4M3) {
+                e4m3x4_to_half2(ws[q], h[2 * q], h[2 * q + 1]);
+              } else {
+                const uint32_t y = ws[q] ^ 0x80808080u;
+                h[2 * q] = biased_bytes_to_half2(y, 0x4140);
+                h[2 * q + 1] = biased_bytes_to_half2(y, 0x4342);
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              __half2 c;
+              memcpy(&c, &h[q], 4);
+              c = __hfma2(c, shi, __hmul2(c, slo));
+              memcpy(&h[q], &c, 4);
+            }
+            const int sw = (first + r0) & 7;
+            *reinterpret_cast<uint4*>(line + first * 128 + ((c0 ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(line + first * 128 + (((c0 + 1) ^ sw) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+          }
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[rs]);
+          mbar_arrive(is_v ? &v_full[s] : &k_full[s]);
+        }
+        r_next += 2;
       }
     }
   } else {
@@ -612,12 +642,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     const float slope = MOD && p.slopes && row_valid ? __ldg(p.slopes + h) * kLog2e : 0.f;
     const float cap_in = MOD && p.softcap > 0.f ? 2.f / p.softcap : 0.f;  // of scores in log2 units
     const float cap_out = p.softcap * kLog2e;
-    const float goff[1] = {0.f};
+    constexpr int NG = kCodes ? 4 : 1;  // groups of keys with an exponent offset of their own
 
     float m_run = -INFINITY, l_run = 0.f;
     for (int jj = 0; jj < n_tiles && ok; ++jj) {
       const int j0 = (j_begin + jj) * BN;
-      const float* sc = sSc + (jj % SR) * 3 * BN;
+      float goff[NG], gsum[NG];
+      uint64_t gx2[NG];
+      goff[0] = 0.f;
+      gx2[0] = xs2;
       if constexpr (kCodes) ok = wait_all(mbar_wait(&sc_full[jj % SR], (jj / SR) & 1, abort_v, p.err));
       if (ok) ok = wait_all(mbar_wait(&s_full[t], jj & 1, abort_v, p.err));
       if (!ok) break;
@@ -630,26 +663,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         tc_fence_before();
         mbar_arrive(&s_free[t]);
       }
-      uint64_t x2[BN / 2];
       if constexpr (kCodes) {
 #pragma unroll
-        for (int c = 0; c < BN; c += 4) {
-          const float4 k4 = *reinterpret_cast<const float4*>(sc + c);
-          const float4 v4 = *reinterpret_cast<const float4*>(sc + BN + c);
-          const uint64_t a = f2_mul(f2u(sr[c], sr[c + 1]), f2(k4.x, k4.y));
-          const uint64_t b = f2_mul(f2u(sr[c + 2], sr[c + 3]), f2(k4.z, k4.w));
-          if constexpr (MOD) {
-            x2[c / 2] = f2_mul(a, xs2);
-            x2[c / 2 + 1] = f2_mul(b, xs2);
-          } else {
-            x2[c / 2] = f2_fma(a, xs2, f2(v4.x, v4.y));
-            x2[c / 2 + 1] = f2_fma(b, xs2, f2(v4.z, v4.w));
-          }
+        for (int y = 0; y < NG; ++y) {
+          const float4 e = sSc[(jj % SR) * 4 + y];
+          gx2[y] = f2(xs * e.x, xs * e.x);
+          goff[y] = e.y;
+          gsum[y] = e.z;
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < BN / 2; ++c) x2[c] = f2_mul(f2u(sr[2 * c], sr[2 * c + 1]), xs2);
       }
+      uint64_t x2[BN / 2];
+#pragma unroll
+      for (int c = 0; c < BN / 2; ++c) x2[c] = f2_mul(f2u(sr[2 * c], sr[2 * c + 1]), gx2[c / (BN / 2 / NG)]);
       if constexpr (MOD) {
         if (p.softcap > 0.f) {  // c tanh(x / c) = c - 2 c / (1 + e^(2 x / c))
 #pragma unroll
@@ -665,14 +690,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         const uint64_t sl2 = f2(slope, slope);
 #pragma unroll
         for (int c = 0; c < BN / 2; ++c) x2[c] = f2_fma(f2(d0 + (float)(2 * c), d0 + (float)(2 * c + 1)), sl2, x2[c]);
-        if constexpr (kCodes) {
-#pragma unroll
-          for (int c = 0; c < BN; c += 4) {
-            const float4 v4 = *reinterpret_cast<const float4*>(sc + BN + c);
-            x2[c / 2] = f2_add(x2[c / 2], f2(v4.x, v4.y));
-            x2[c / 2 + 1] = f2_add(x2[c / 2 + 1], f2(v4.z, v4.w));
-          }
-        }
       }
       if (!(j0 >= lo_i && j0 + BN <= hi_i)) {
 #pragma unroll
@@ -684,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             x2[c / 2] = f2(lo, hi);
           }
       }
-      const float mx = tile::row_max<1, BN>(x2, goff);
+      const float mx = tile::row_max<NG, BN / NG>(x2, goff);
       const float m_new = fmaxf(m_run, mx);
       const bool need = m_new > m_run + kLag;
       float alpha = 1.f;
@@ -696,26 +713,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       const float m_use = m_run == -INFINITY ? 0.f : m_run - kOffset;
       uint32_t pk[BN / 2];
       if constexpr (kCodes) {
-        const uint64_t nm = f2(-m_use, -m_use);
-        uint64_t sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < BN; c += 4) {
-          const float4 i4 = *reinterpret_cast<const float4*>(sc + 2 * BN + c);
-          float w[4];
-          f2_split(f2_add(x2[c / 2], nm), w[0], w[1]);
-          f2_split(f2_add(x2[c / 2 + 1], nm), w[2], w[3]);
+        for (int y = 0; y < NG; ++y) {
+          const float no = goff[y] - m_use;
+          const uint64_t no2 = f2(no, no);
+          uint64_t sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) w[q] = ex2_approx(w[q]);
-          sum[0] = f2_fma(f2(w[0], w[1]), f2(i4.x, i4.y), sum[0]);
-          sum[1] = f2_fma(f2(w[2], w[3]), f2(i4.z, i4.w), sum[1]);
-          const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
-          memcpy(&pk[c / 2], &h0, 4);
-          memcpy(&pk[c / 2 + 1], &h1, 4);
+          for (int c = y * BN / 2 / NG; c < (y + 1) * BN / 2 / NG; ++c) {
+            float lo, hi;
+            f2_split(f2_add(x2[c], no2), lo, hi);
+            lo = ex2_approx(lo);
+            hi = ex2_approx(hi);
+            sum[c & 1] = f2_add(sum[c & 1], f2(lo, hi));
+            const __half2 hh = __floats2half2_rn(lo, hi);
+            memcpy(&pk[c], &hh, 4);
+          }
+          float a0, a1, b0, b1;
+          f2_split(sum[0], a0, a1);
+          f2_split(sum[1], b0, b1);
+          l_run = fmaf((a0 + a1) + (b0 + b1), gsum[y], l_run);
         }
-        float a0, a1, b0, b1;
-        f2_split(sum[0], a0, a1);
-        f2_split(sum[1], b0, b1);
-        l_run += (a0 + a1) + (b0 + b1);
       } else {
         l_run += tile::exp_pack<BN, BN>(x2, goff, m_use, pk);
       }
@@ -785,15 +802,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
 
 // Adds the parts of a unit's rows, O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i:
 // a block has 32 rows of a unit, a thread 16 columns of one.
+constexpr int kMergeThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(kThreads) paged_tc_merge_kernel(const __grid_constant__ TcPagedArgs args) {
+__global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const __grid_constant__ TcPagedArgs args) {
   const PagedParams& p = args.p;
   grid_dep_wait();
   grid_dep_launch();
   const int unit = blockIdx.x >> 3;
   TcUnit u;
-  if (!find_unit(args, unit, u)) return;
-  for (int x = threadIdx.x; x < 32 * (D / 16); x += kThreads) {
+  if (!find_unit<kMergeThreads>(args, unit, u)) return;
+  for (int x = threadIdx.x; x < 32 * (D / 16); x += kMergeThreads) {
     const int row = (blockIdx.x & 7) * 32 + (x & 31), c0 = (x >> 5) * 4;  // first of 4 float4 columns
     const int t = row >> 7, lr = row & 127;
     const int tk = (int)fdiv((uint32_t)lr, args.fd_g), g = lr - tk * p.group;
@@ -897,14 +915,14 @@ cudaError_t tc_one(const TcPagedArgs& a, bool mod, long long units, cudaStream_t
       // launch only what was compiled to the count the split assumes
       cudaFuncAttributes fa;
       if (bad[mod] == cudaSuccess) bad[mod] = cudaFuncGetAttributes(&fa, kern);
-      if (bad[mod] == cudaSuccess && fa.numRegs != kRegsLaunch) bad[mod] = cudaErrorInvalidConfiguration;
+      if (bad[mod] == cudaSuccess && fa.numRegs != kRegsLaunch<KV>) bad[mod] = cudaErrorInvalidConfiguration;
       if (bad[mod] == cudaSuccess) done[mod] |= 1ull << (dev & 63);
     }
     if (bad[mod] != cudaSuccess) return bad[mod];
   }
-  cudaError_t e = launch_serialized(kern, dim3((unsigned)(units * a.n_split)), dim3(kThreads), (size_t)L::kAlloc, stream, a);
+  cudaError_t e = launch_serialized(kern, dim3((unsigned)(units * a.n_split)), dim3(kThreadsOf<KV>), (size_t)L::kAlloc, stream, a);
   if (e != cudaSuccess || a.n_split == 1) return e;
-  return launch_serialized(paged_tc_merge_kernel<D>, dim3((unsigned)(units * 8)), dim3(kThreads), 0, stream, a);
+  return launch_serialized(paged_tc_merge_kernel<D>, dim3((unsigned)(units * 8)), dim3(kMergeThreads), 0, stream, a);
 }
 
 }  // namespace

@@ -86,7 +86,7 @@ class Pool:
         return self.val[which][self.table[b, j // self.page].long(), :, j % self.page].transpose(0, 1)
 
 
-def attend(pool, q, n, *, scale=None, window=0, softcap=0.0, slopes=None, u_p=0.0, p_floor=0.0):
+def attend(pool, q, n, *, scale=None, window=0, softcap=0.0, slopes=None, u_p=0.0, p_floor=0.0, u_kv=0.0):
     """(out, lse, bound on |out|'s error without its own rounding, bound on
     lse's) in 64 bits for packed rows q [sum n, Hq, d].
 
@@ -101,7 +101,16 @@ def attend(pool, q, n, *, scale=None, window=0, softcap=0.0, slopes=None, u_p=0.
     the largest P at 2^12 or more: 2^-37 of the largest.  P there stands for
     2^t, t_j = x_j log2 e + log2 vs_j, and multiplies codes c_j, so the sum of
     p_j c_j is off by at most p_floor 2^tmax sum |c_j|; it is divided by sum
-    2^t_j / vs_j >= 2^tmax / vs_(argmax t): p_floor vs_(argmax t) sum |c_j|."""
+    2^t_j / vs_j >= 2^tmax / vs_(argmax t): p_floor vs_(argmax t) sum |c_j|.
+
+    u_kv: where dequantised keys and values are rounded to f16 (codes times a
+    scale relative to a power of two of 32 keys).  A score is off by u_kv scale
+    sum |q k| more, the value sum by u_kv sum p |v|.  P then multiplies
+    v_j 2^-ev_j, with 2^ev_j at most the largest scale of j's 32 keys / 64 and
+    at least vs_j / 128, so the floor's share is at most p_floor 2^ev sum |v_j|
+    2^-ev_j <= p_floor (max vs / 64) sum 128 |c_j| = 2 p_floor max vs sum |c_j|.
+    (A value below 2^-30 of its 32 keys' largest is off by 2^-40 of that largest
+    at most, which the fp32 terms cover.)"""
     T, Hq, d = q.shape
     q = q.double()
     scale = 1.0 / math.sqrt(d) if scale is None else scale
@@ -129,7 +138,7 @@ def attend(pool, q, n, *, scale=None, window=0, softcap=0.0, slopes=None, u_p=0.
                     x = softcap * torch.tanh(x / softcap)
                 if slopes is not None:
                     x = x + slopes[h].double() * (j - pos)
-                e = 2.0 ** -23 * ((d + 8) * size + 8 * x.abs() + 4 * softcap + 4)
+                e = u_kv * size + 2.0 ** -23 * ((d + 8) * size + 8 * x.abs() + 4 * softcap + 4)
                 x = x.masked_fill(hidden, -math.inf)
                 top = x.amax(-1, keepdim=True)
                 ok = torch.isfinite(top[:, 0])
@@ -140,12 +149,13 @@ def attend(pool, q, n, *, scale=None, window=0, softcap=0.0, slopes=None, u_p=0.
                 lse[at:at + m, h] = torch.where(ok, top[:, 0] + den[:, 0].log(), torch.full((), -math.inf))
                 pe = p * (2 * e)
                 acc = (L / 8 + 64) * 2.0 ** -23
-                tol[at:at + m, h] = (pe + (u_p + acc) * p) @ vv.abs() + (pe.sum(-1, keepdim=True) + acc) * out[at:at + m, h].abs()
+                tol[at:at + m, h] = (pe + (u_p + u_kv + acc) * p) @ vv.abs() + (pe.sum(-1, keepdim=True) + acc) * out[at:at + m, h].abs()
                 if p_floor:
                     vs = pool.scales[1].double()[pool.table[b, j[0] // pool.page].long(), h // G, j[0] % pool.page]
                     t = x / math.log(2.0) + vs.log2()
                     size_c = (~hidden).double() @ (vv / vs[:, None]).abs()
-                    tol[at:at + m, h] += p_floor * vs[t.argmax(-1)][:, None] * size_c
+                    top_vs = 2 * vs.max() if u_kv else vs[t.argmax(-1)][:, None]
+                    tol[at:at + m, h] += p_floor * top_vs * size_c
                 ltol[at:at + m, h] = pe.sum(-1) + acc + 2.0 ** -22 * lse[at:at + m, h].abs().nan_to_num(posinf=0)
         at += m
     return out, lse, tol, ltol

@@ -148,7 +148,8 @@ def run_case(path, cdt, io, Hq, Hkv, d, page, kv, n, *, layout="hnd", window=0, 
     rounded = path != "exact" and io == BF16  # P is f16 beside codes, else bf16
     want, wlse, tol, ltol = R.attend(pool, q, rows, scale=scale, window=window, softcap=softcap, slopes=sl,
                                      u_p=R.U[torch.float16 if codes else BF16] if rounded else 0.0,
-                                     p_floor=2.0 ** -37 if rounded and codes else 0.0)
+                                     p_floor=2.0 ** -37 if rounded and codes else 0.0,
+                                     u_kv=R.U[torch.float16] if codes and path in ("tcgen05", "auto") and io == BF16 else 0.0)
     what = f"{path} {cdt} {Hq}/{Hkv} d{d} page {page} kv {kv} n {n} w{window} c{softcap} s{slopes}"
     R.check(out, want, tol, io, what)
     R.check_lse(lse, wlse, ltol, what)
