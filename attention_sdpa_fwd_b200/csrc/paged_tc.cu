@@ -170,7 +170,26 @@ __device__ __forceinline__ bool find_unit(const TcPagedArgs& a, int unit, TcUnit
   return true;
 }
 
-template <int KV, int D, bool MOD>
+// Four scores x in log2 units to c tanh(x / c) = c - 2 c / (1 + 2^(2 x / c)),
+// one reciprocal for the four: 1 / a = b c d / (a b c d).  The exponent is kept
+// below 30, where tanh is 1 - 2^-29, so that the product stays finite.
+// (The multi-function unit bounds capped scores: 2.25 operations a score
+// instead of 3.)
+__device__ __forceinline__ void cap4(uint64_t& x, uint64_t& y, float cap_in, float cap_out) {
+  float v[4], a[4];
+  f2_split(x, v[0], v[1]);
+  f2_split(y, v[2], v[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = 1.f + ex2_approx(fminf(v[i] * cap_in, 30.f));
+  const float ab = a[0] * a[1], cd = a[2] * a[3];
+  const float r = rcp_approx(ab * cd) * (-2.f * cap_out);
+  const float rab = r * cd, rcd = r * ab;
+  x = f2(fmaf(rab, a[1], cap_out), fmaf(rab, a[0], cap_out));
+  y = f2(fmaf(rcd, a[3], cap_out), fmaf(rcd, a[2], cap_out));
+}
+
+// MOD: 0 plain scores, 1 with slopes, 2 capped (and with slopes, which may be zero).
+template <int KV, int D, int MOD>
 __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __grid_constant__ TcPagedArgs args) {
   using L = TcLayout<KV, D>;
   constexpr bool kCodes = L::kCodes;
@@ -640,17 +659,21 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
     }
     const uint64_t xs2 = f2(xs, xs);
     const float slope = MOD && p.slopes && row_valid ? __ldg(p.slopes + h) * kLog2e : 0.f;
-    const float cap_in = MOD && p.softcap > 0.f ? 2.f / p.softcap : 0.f;  // of scores in log2 units
+    const float cap_in = MOD == 2 ? 2.f / p.softcap : 0.f;  // of scores in log2 units
     const float cap_out = p.softcap * kLog2e;
-    constexpr int NG = kCodes ? 4 : 1;  // groups of keys with an exponent offset of their own
+    // groups of keys with an exponent offset of their own: V's scales, the slope's part of a group
+    constexpr int NG = kCodes || MOD ? 4 : 1;
 
     float m_run = -INFINITY, l_run = 0.f;
     for (int jj = 0; jj < n_tiles && ok; ++jj) {
       const int j0 = (j_begin + jj) * BN;
       float goff[NG], gsum[NG];
       uint64_t gx2[NG];
-      goff[0] = 0.f;
-      gx2[0] = xs2;
+#pragma unroll
+      for (int y = 0; y < NG; ++y) {
+        goff[y] = MOD ? slope * (float)(j0 - pos + y * (BN / NG)) : 0.f;
+        gx2[y] = xs2;
+      }
       if constexpr (kCodes) ok = wait_all(mbar_wait(&sc_full[jj % SR], (jj / SR) & 1, abort_v, p.err));
       if (ok) ok = wait_all(mbar_wait(&s_full[t], jj & 1, abort_v, p.err));
       if (!ok) break;
@@ -668,28 +691,34 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
         for (int y = 0; y < NG; ++y) {
           const float4 e = sSc[(jj % SR) * 4 + y];
           gx2[y] = f2(xs * e.x, xs * e.x);
-          goff[y] = e.y;
+          goff[y] += e.y;
           gsum[y] = e.z;
         }
       }
+      // slopes: (j - pos) slope = a group's first key's, in goff, + 0, slope, 2 slope ..
+      // over the group, a running sum (32 steps: the fp32 rounding of the scores)
       uint64_t x2[BN / 2];
 #pragma unroll
-      for (int c = 0; c < BN / 2; ++c) x2[c] = f2_mul(f2u(sr[2 * c], sr[2 * c + 1]), gx2[c / (BN / 2 / NG)]);
-      if constexpr (MOD) {
-        if (p.softcap > 0.f) {  // c tanh(x / c) = c - 2 c / (1 + e^(2 x / c))
+      for (int y = 0; y < NG; ++y) {
+        uint64_t ramp = f2(0.f, slope);
+        const uint64_t two = f2(2.f * slope, 2.f * slope);
 #pragma unroll
-          for (int c = 0; c < BN / 2; ++c) {
-            float lo, hi;
-            f2_split(x2[c], lo, hi);
-            lo = fmaf(-2.f * cap_out, rcp_approx(1.f + ex2_approx(lo * cap_in)), cap_out);
-            hi = fmaf(-2.f * cap_out, rcp_approx(1.f + ex2_approx(hi * cap_in)), cap_out);
-            x2[c] = f2(lo, hi);
+        for (int c = y * BN / 2 / NG; c < (y + 1) * BN / 2 / NG; ++c) {
+          const uint64_t s2 = f2u(sr[2 * c], sr[2 * c + 1]);
+          if constexpr (MOD == 0) x2[c] = f2_mul(s2, gx2[y]);
+          if constexpr (MOD == 1) x2[c] = f2_fma(s2, gx2[y], ramp);
+          if constexpr (MOD == 2) {
+            x2[c] = f2_mul(s2, gx2[y]);
+            if (c & 1) {
+              cap4(x2[c - 1], x2[c], cap_in, cap_out);
+              x2[c - 1] = f2_add(x2[c - 1], ramp);
+              ramp = f2_add(ramp, two);
+              x2[c] = f2_add(x2[c], ramp);
+              ramp = f2_add(ramp, two);
+            }
           }
+          if constexpr (MOD == 1) ramp = f2_add(ramp, two);
         }
-        const float d0 = (float)(j0 - pos);
-        const uint64_t sl2 = f2(slope, slope);
-#pragma unroll
-        for (int c = 0; c < BN / 2; ++c) x2[c] = f2_fma(f2(d0 + (float)(2 * c), d0 + (float)(2 * c + 1)), sl2, x2[c]);
       }
       if (!(j0 >= lo_i && j0 + BN <= hi_i)) {
 #pragma unroll
@@ -734,7 +763,7 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
           l_run = fmaf((a0 + a1) + (b0 + b1), gsum[y], l_run);
         }
       } else {
-        l_run += tile::exp_pack<BN, BN>(x2, goff, m_use, pk);
+        l_run += tile::exp_pack<BN, BN / NG>(x2, goff, m_use, pk);
       }
       if constexpr (kPSep) {
         if (jj > 0) {
@@ -898,12 +927,12 @@ bool q_map(CUtensorMap* m, const PagedParams& p, int tok) {
 }
 
 template <int KV, int D>
-cudaError_t tc_one(const TcPagedArgs& a, bool mod, long long units, cudaStream_t stream) {
+cudaError_t tc_one(const TcPagedArgs& a, int mod, long long units, cudaStream_t stream) {
   using L = TcLayout<KV, D>;
-  auto kern = mod ? paged_tc_kernel<KV, D, true> : paged_tc_kernel<KV, D, false>;
+  auto kern = mod == 0 ? paged_tc_kernel<KV, D, 0> : mod == 1 ? paged_tc_kernel<KV, D, 1> : paged_tc_kernel<KV, D, 2>;
   static std::mutex mu;
-  static uint64_t done[2];
-  static cudaError_t bad[2];
+  static uint64_t done[3];
+  static cudaError_t bad[3];
   {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -982,7 +1011,7 @@ cudaError_t launch_paged_tc(const PagedParams& p, int limit, void* ws, cudaStrea
     a.ws_o = static_cast<float*>(ws);
     a.ws_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + up256(parts * 256 * c.d * 4));
   }
-  const bool mod = p.softcap > 0.f || p.slopes != nullptr;
+  const int mod = p.softcap > 0.f ? 2 : p.slopes != nullptr ? 1 : 0;
   const bool wide = c.d == 128;
   switch (c.dtype) {
     case SDPA_CACHE_BF16: return wide ? tc_one<KV_BF16, 128>(a, mod, units, stream) : tc_one<KV_BF16, 64>(a, mod, units, stream);
