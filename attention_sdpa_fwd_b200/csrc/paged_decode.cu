@@ -5,16 +5,17 @@
 // (row, key) are far below what the bytes leave room for.  So the work is laid
 // out by bytes, not by sequences:
 //
-//  * Work is counted in tiles of kWarps * KS keys of one (sequence, kv head),
+//  * Work is counted in tiles of KS keys per stream of one (sequence, kv head),
 //    all units in one row; CTA c of G takes tiles [T c / G, T (c+1) / G), T from
 //    a scan of the lengths at its start.  Every CTA streams the same number of
 //    bytes whatever the lengths are.  A unit that ends up in several CTAs
 //    leaves unnormalised parts (O, max, sum) in the workspace, at most two per
 //    CTA, and merge_kernel, launched behind, adds them in a fixed order: no
 //    atomics, no state between calls.
-//  * Each warp runs on its own: it copies KS keys and values at a time with
+//  * Each warp runs on its own (two together where a unit has more than 16
+//    rows, a row tile each): it copies KS keys and values at a time with
 //    16-byte cp.async into its own ring of NST stages and never waits for
-//    another warp before the end of a unit.  Keys outside the visible range are
+//    other warps before the end of a unit.  Keys outside the visible range are
 //    filled with zeros without being read (their pages may be gone).
 //  * S = Q.K^T and O += P.V are mma.sync m16n8k16 tiles: at this arithmetic
 //    intensity the tensor pipe is far from its limit and register fragments
@@ -65,32 +66,34 @@ struct DecodeArgs {
   int whole;   // one CTA per unit, nothing split
   float* ws_o;      // [2 * CTAs][rows][D]
   float2* ws_ml;    // [2 * CTAs][rows]
-  long long* ws_first;  // [units] first tile of a unit in the row of all tiles
-  long long* ws_hdr;  // T, CTAs that have work
+  int4* ws_unit;    // [units] CTAs that share a unit: first, last, slot of the first (0 or 1)
 };
 
+// MT: 16-row tiles of a unit.  MT warps share a stream of keys, a row tile each.
 template <int KV, int D, int MT>
 struct Cfg {
-  static constexpr int kElem = KV == KV_BF16 ? 2 : 1;
-  static constexpr int KS = KV == KV_BF16 ? (D == 128 ? 16 : 32) : 32;  // keys of a warp's step
-  static constexpr int SB = MT == 1 ? KS : 16;                          // keys of one softmax update
+  static constexpr bool kCodes = KV != KV_BF16;
+  static constexpr int kElem = kCodes ? 1 : 2;
+  static constexpr int kStreams = kWarps / MT;
+  static constexpr int KS = !kCodes && D == 128 ? 16 : 32;       // keys of a stream's step
   static constexpr int kRow = D * kElem;
-  static constexpr int kTile = KS * kRow;                               // K (or V) of a step
-  static constexpr int kScales = KV == KV_BF16 ? 0 : 4 * KS * 4;        // ks, vs, log2 vs, 1 / vs
+  static constexpr int kTile = KS * kRow;                        // K (or V) of a step
+  static constexpr int kScales = kCodes ? 4 * KS * 4 : 0;        // ks, vs, log2 vs, 1 / vs
   static constexpr int kStage = 2 * kTile + kScales;
-  static constexpr bool kQSmem = MT > 1 || KV != KV_BF16;               // Q fragments in shared memory
-  static constexpr int kCtas = MT == 1 && KV != KV_BF16 ? 3 : 2;        // of an SM
-  static constexpr int NST = KV == KV_BF16 ? 3 : MT > 1 ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 3);
+  static constexpr bool kQSmem = kCodes;                         // Q fragments in shared memory
+  static constexpr int kCtas = kCodes ? 3 : 2;                   // of an SM
+  static constexpr int NST = kCodes ? (D == 128 ? 1 + MT : 3) : 3 * MT;
   static constexpr int kRows = 16 * MT;
   static constexpr int kPitch = D + 4;
-  static constexpr int kRing = kWarps * NST * kStage;
-  static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
+  static constexpr int kRing = kStreams * NST * kStage;
+  static constexpr int kMergeBytes = kStreams * kRows * kPitch * 4;
   static constexpr int kQ = kQSmem ? MT * (D / 16) * 32 * 16 : 0;
   static constexpr int kBig = kRing > kMergeBytes ? kRing : kMergeBytes;
   static constexpr int oQ = kBig;
-  static constexpr int oML = oQ + kQ;                                   // [kWarps][kRows] float2
-  static constexpr int kTotal = oML + kWarps * kRows * 8;
-  static constexpr int kKeys = kWarps * KS;                             // keys of a tile
+  static constexpr int oML = oQ + kQ;                            // [kStreams][kRows] float2
+  static constexpr int kTotal = oML + kStreams * kRows * 8;
+  static constexpr int kKeys = kStreams * KS;                    // keys of a tile
+  static_assert(kCtas * (kTotal + 1024) <= 233472, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
@@ -192,7 +195,7 @@ template <int KV, int D, int MT, bool MOD>
 __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decode_kernel(const __grid_constant__ DecodeArgs a) {
   using C = Cfg<KV, D, MT>;
   constexpr bool F16 = KV != KV_BF16;
-  constexpr int KS = C::KS, SB = C::SB, NST = C::NST;
+  constexpr int KS = C::KS, NST = C::NST;
   constexpr float kShift = kOffset<F16>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_b;
@@ -200,6 +203,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
   const PagedParams& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quad = lane >> 2, c = lane & 3;
+  const int stream = warp / MT, rt = warp % MT;  // stream of keys, row tile
+  auto stream_sync = [&] {
+    if constexpr (MT == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + stream), "n"(32 * MT) : "memory");
+  };
   grid_dep_wait();
   grid_dep_launch();  // the merge may start: it reads nothing of this call's inputs that still changes
 
@@ -254,14 +262,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
     __syncthreads();
     b = s_b;
     F = s_F;
-    if (blockIdx.x == 0 && tid == 0) {
-      a.ws_hdr[0] = T;
-      a.ws_hdr[1] = work_ctas;
-    }
   }
   const long long begin = cur;
 
-  const uint32_t ring = smem_u32(smem) + warp * (NST * C::kStage);
+  const uint32_t ring = smem_u32(smem) + stream * (NST * C::kStage);
   float* mrg = reinterpret_cast<float*>(smem);
   float2* s_ml = reinterpret_cast<float2*>(smem + C::oML);
 
@@ -271,15 +275,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
     const int hk = (int)div64(cur - F, u.nt);
     const int tile0 = (int)((cur - F) - (long long)hk * u.nt);
     const int ntile = (int)min((long long)(u.nt - tile0), end - cur);
-    const int base = u.lo16 + tile0 * C::kKeys + warp * KS;  // this warp's first key
+    const int base = u.lo16 + tile0 * C::kKeys + stream * KS;  // this stream's first key
     const int khi = u.hi, klo = u.lo;
 
-    // ---- the ring: one step is KS keys and values of this warp
+    // ---- the ring: one step is KS keys and values of this stream, each of its warps copies a share of the rows
     const uint8_t* kp = static_cast<const uint8_t*>(p.c.k) + (long long)hk * p.c.kh * C::kElem;
     const uint8_t* vp = static_cast<const uint8_t*>(p.c.v) + (long long)hk * p.c.vh * C::kElem;
     constexpr int kPieces = C::kRow / 16;  // of a row
-    constexpr int kPass = 32 / kPieces;    // rows the warp copies at once
-    const int piece = lane % kPieces, r0 = lane / kPieces;
+    constexpr int kPass = MT * 32 / kPieces;  // rows the stream's warps copy at once
+    const int piece = lane % kPieces, r0 = rt * (32 / kPieces) + lane / kPieces;
     const long long kstep = p.c.kt * (kPass * C::kElem), vstep = p.c.vt * (kPass * C::kElem);
     kp += (long long)r0 * p.c.kt * C::kElem + piece * 16;
     vp += (long long)r0 * p.c.vt * C::kElem + piece * 16;
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
           kq[g] += kstep;
           vq[g] += vstep;
         }
-        if constexpr (F16) {  // KS == 32: a lane per key
+        if (F16 && rt == 0) {  // KS == 32: a lane per key
           const bool live = all || (t0 + lane >= klo && t0 + lane < khi);
           const uint32_t sc = st + 2 * C::kTile + lane * 4;
           cp4(sc, ksq, live);
@@ -348,87 +352,81 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
 
     // ---- Q as A fragments: row r of the unit is token r / group, head r % group
     uint32_t qf[C::kQSmem ? 1 : D / 16][4];
-    float xscale[MT][2];  // what turns the accumulator of a row into its score
-    int pos[MT][2];
-    float slope[MT][2];
+    float xscale[2];  // what turns the accumulator of a row into its score
+    int pos[2];
+    float slope[2];
     const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(p.q);
-    uint32_t* s_q = reinterpret_cast<uint32_t*>(smem + C::oQ);
+    uint32_t* s_q = reinterpret_cast<uint32_t*>(smem + C::oQ) + rt * (D / 16) * 128;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int e = 0; e < 2; ++e) {
+      const int r = rt * 16 + e * 8 + quad;
+      const int i = r / p.group, g = r - i * p.group;
+      const bool live = r < u.rows;
+      const int h = hk * p.group + g;
+      const __nv_bfloat16* src = qb + (long long)(u.s.q0 + i) * p.qt + (long long)h * p.qh;
+      pos[e] = u.s.L - u.s.n + i;
+      slope[e] = MOD && p.slopes && live ? __ldg(p.slopes + h) : 0.f;
+      xscale[e] = p.scale;
+      uint32_t w[D / 8];  // this lane's D / 4 elements, in pairs
+      if constexpr (F16) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = m * 16 + e * 8 + quad;
-        const int i = r / p.group, g = r - i * p.group;
-        const bool live = r < u.rows;
-        const int h = hk * p.group + g;
-        const __nv_bfloat16* src = qb + (long long)(u.s.q0 + i) * p.qt + (long long)h * p.qh;
-        pos[m][e] = u.s.L - u.s.n + i;
-        slope[m][e] = MOD && p.slopes && live ? __ldg(p.slopes + h) : 0.f;
-        xscale[m][e] = p.scale;
-        uint32_t w[D / 8];  // this lane's D / 4 elements, in pairs
-        if constexpr (F16) {
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (live) x = *reinterpret_cast<const uint4*>(src + c * (D / 4) + k * 8);
-            w[4 * k] = x.x; w[4 * k + 1] = x.y; w[4 * k + 2] = x.z; w[4 * k + 3] = x.w;
-          }
-          float top = 0.f;
-#pragma unroll
-          for (int k = 0; k < D / 8; ++k)
-            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // 2^k with top 2^k in [2^14, 2^15), k within what a float holds
-          const int ex = top > 0.f && top < INFINITY ? min(126, max(-126, 141 - (int)(__float_as_uint(top) >> 23))) : 0;
-          const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
-          xscale[m][e] *= __uint_as_float((uint32_t)(127 - ex) << 23);
-#pragma unroll
-          for (int k = 0; k < D / 8; ++k) {
-            const __half2 hh = __floats2half2_rn(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
-            memcpy(&w[k], &hh, 4);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < D / 8; ++k)
-            w[k] = live ? __ldg(reinterpret_cast<const unsigned int*>(src + 16 * (k >> 1) + 8 * (k & 1) + 2 * c)) : 0u;
+        for (int k = 0; k < D / 32; ++k) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (live) x = *reinterpret_cast<const uint4*>(src + c * (D / 4) + k * 8);
+          w[4 * k] = x.x; w[4 * k + 1] = x.y; w[4 * k + 2] = x.z; w[4 * k + 3] = x.w;
         }
-        // pair 2s is a0 / a1 of k-step s, pair 2s + 1 is a2 / a3
+        float top = 0.f;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          if constexpr (!C::kQSmem) {
-            qf[s][e] = w[2 * s];
-            qf[s][2 + e] = w[2 * s + 1];
-          } else if (s % kWarps == warp) {  // every warp has the same fragments: each writes a share
-            s_q[((m * (D / 16) + s) * 32 + lane) * 4 + e] = w[2 * s];
-            s_q[((m * (D / 16) + s) * 32 + lane) * 4 + 2 + e] = w[2 * s + 1];
-          }
+        for (int k = 0; k < D / 8; ++k)
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^k with top 2^k in [2^14, 2^15), k within what a float holds
+        const int ex = top > 0.f && top < INFINITY ? min(126, max(-126, 141 - (int)(__float_as_uint(top) >> 23))) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+        xscale[e] *= __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const __half2 hh = __floats2half2_rn(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
+          memcpy(&w[k], &hh, 4);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k)
+          w[k] = live ? __ldg(reinterpret_cast<const unsigned int*>(src + 16 * (k >> 1) + 8 * (k & 1) + 2 * c)) : 0u;
+      }
+      // pair 2s is a0 / a1 of k-step s, pair 2s + 1 is a2 / a3
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        if constexpr (!C::kQSmem) {
+          qf[s][e] = w[2 * s];
+          qf[s][2 + e] = w[2 * s + 1];
+        } else if (s % C::kStreams == stream) {  // the streams' warps of a row tile have the same: each writes a share
+          s_q[(s * 32 + lane) * 4 + e] = w[2 * s];
+          s_q[(s * 32 + lane) * 4 + 2 + e] = w[2 * s + 1];
         }
       }
     }
     if constexpr (C::kQSmem) __syncthreads();
 
-    float o[MT][D / 8][4];
-    float mx[MT][2], l[MT][2];
+    float o[D / 8][4];
+    float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[m][i][k] = 0.f;
-      mx[m][0] = mx[m][1] = -INFINITY;
-      l[m][0] = l[m][1] = 0.f;
-    }
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
     const int pos_first = u.s.L - u.s.n, pos_last = u.s.L - 1;
     const float icap2 = MOD && p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
 
     for (int step = 0; step < ntile; ++step) {
       cp_wait<NST - 2>();
-      __syncwarp();
+      stream_sync();
       const uint32_t st = ring + (step % NST) * C::kStage;
       const int t0 = base + step * C::kKeys;
       float* sc = reinterpret_cast<float*>(smem + (st - smem_u32(smem)) + 2 * C::kTile);
-      if constexpr (F16) {  // log2 vs and 1 / vs of this lane's key; a key not read counts as scale 1
+      if constexpr (F16) {
+        // log2 vs and 1 / vs of this lane's key (every warp of the stream
+        // writes the same); a key not read counts as scale 1
         const int t = t0 + lane;
         const float vs = t >= klo && t < khi ? sc[KS + lane] : 1.f;
         float lg;
@@ -441,259 +439,209 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
       if (t0 >= khi || t0 + KS <= klo) continue;  // nothing of it is seen
       if constexpr (F16) __syncwarp();
       const bool edge = t0 + KS - 1 > pos_first || t0 < klo || (p.window > 0 && t0 <= pos_last - p.window);
+      // ---- S = Q.K^T
+      float s[KS / 8][4];
 #pragma unroll
-      for (int sb = 0; sb < KS; sb += SB) {
-        // ---- S = Q.K^T
-        float s[MT][SB / 8][4];
+      for (int n = 0; n < KS / 8; ++n)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
+      if constexpr (F16) {
+        uint32_t w[KS / 8][D / 16];
 #pragma unroll
-          for (int n = 0; n < SB / 8; ++n)
+        for (int n = 0; n < KS / 8; ++n)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[m][n][k] = 0.f;
+          for (int i = 0; i < D / 64; ++i) {
+            const uint4 x = lds16(st + k_off<KV, D>(n * 8 + quad, c * (D / 64) + i));
+            w[n][4 * i] = x.x; w[n][4 * i + 1] = x.y; w[n][4 * i + 2] = x.z; w[n][4 * i + 3] = x.w;
+          }
+#pragma unroll
+        for (int ss = 0; ss < D / 16; ++ss) {
+          const uint4 x = lds16(smem_u32(s_q) + (ss * 32 + lane) * 16);
+          const uint32_t q4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int n = 0; n < KS / 8; ++n) {
+            uint32_t b0, b1;
+            codes4<KV>(w[n][ss], b0, b1);
+            mma<F16>(s[n], q4, b0, b1);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int sp = 0; sp < D / 32; ++sp)
+#pragma unroll
+          for (int n = 0; n < KS / 8; ++n) {
+            uint32_t r[4];
+            ldsm4(st + k_off<KV, D>(n * 8 + (lane & 7), 4 * sp + (lane >> 3)), r);
+            mma<F16>(s[n], qf[2 * sp], r[0], r[1]);
+            mma<F16>(s[n], qf[2 * sp + 1], r[2], r[3]);
+          }
+      }
+      // ---- scores in log2 units, running max, P
+      uint32_t pf[KS / 16][4];
+      float iv[F16 ? KS / 8 : 1][2];
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < KS / 8; ++n) {
+        const int kk = n * 8 + 2 * c;
+        float ks2[2] = {1.f, 1.f}, lv2[2] = {0.f, 0.f};
         if constexpr (F16) {
-          uint32_t w[SB / 8][D / 16];
+          const float2 x = *reinterpret_cast<const float2*>(sc + kk);
+          const float2 y = *reinterpret_cast<const float2*>(sc + 2 * KS + kk);
+          const float2 z = *reinterpret_cast<const float2*>(sc + 3 * KS + kk);
+          ks2[0] = x.x; ks2[1] = x.y; lv2[0] = y.x; lv2[1] = y.y;
+          iv[n][0] = z.x; iv[n][1] = z.y;
+        }
 #pragma unroll
-          for (int n = 0; n < SB / 8; ++n)
+        for (int k = 0; k < 4; ++k) {
+          const int e = k >> 1, j = t0 + kk + (k & 1);
+          if constexpr (MOD) {
+            float y = s[n][k] * xscale[e] * ks2[k & 1];
+            if (p.softcap > 0.f)  // c tanh(y / c) = c - 2 c / (1 + e^(2 y / c))
+              y = fmaf(-2.f * p.softcap, rcp_approx(1.f + ex2_approx(y * icap2)), p.softcap);
+            y = fmaf(slope[e], (float)(j - pos[e]), y);
+            s[n][k] = fmaf(y, kLog2e, lv2[k & 1]);
+          } else if constexpr (F16) {
+            s[n][k] = fmaf(s[n][k] * ks2[k & 1], xscale[e] * kLog2e, lv2[k & 1]);
+          } else {
+            s[n][k] *= xscale[e] * kLog2e;
+          }
+        }
+      }
+      if (edge) {
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-              const uint4 x = lds16(st + k_off<KV, D>(sb + n * 8 + quad, c * (D / 64) + i));
-              w[n][4 * i] = x.x; w[n][4 * i + 1] = x.y; w[n][4 * i + 2] = x.z; w[n][4 * i + 3] = x.w;
+        for (int n = 0; n < KS / 8; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = t0 + n * 8 + 2 * c + (k & 1);
+            if (j > pos[k >> 1] || (p.window > 0 && j <= pos[k >> 1] - p.window)) s[n][k] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < KS / 8; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[k >> 1] = fmaxf(top[k >> 1], s[n][k]);
+      bool grow = false;
+      float al[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+        al[e] = 1.f;
+        if (top[e] > mx[e] + kLag<F16>) {  // from -inf too; false while both are
+          al[e] = ex2_approx(mx[e] - top[e]);
+          mx[e] = top[e];
+          grow = true;
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        l[0] *= al[0];
+        l[1] *= al[1];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= al[0]; o[i][1] *= al[0];
+          o[i][2] *= al[1]; o[i][3] *= al[1];
+        }
+      }
+      const float ms[2] = {mx[0] == -INFINITY ? 0.f : mx[0] - kShift, mx[1] == -INFINITY ? 0.f : mx[1] - kShift};
+#pragma unroll
+      for (int n = 0; n < KS / 8; ++n) {
+        float w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          w[k] = ex2_approx(s[n][k] - ms[k >> 1]);
+          if constexpr (F16) l[k >> 1] = fmaf(w[k], iv[n][k & 1], l[k >> 1]);
+          else l[k >> 1] += w[k];
+        }
+        if constexpr (F16) {
+          const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
+          memcpy(&pf[n >> 1][(n & 1) * 2], &h0, 4);
+          memcpy(&pf[n >> 1][(n & 1) * 2 + 1], &h1, 4);
+        } else {
+          pf[n >> 1][(n & 1) * 2] = pack_bf16x2(w[0], w[1]);
+          pf[n >> 1][(n & 1) * 2 + 1] = pack_bf16x2(w[2], w[3]);
+        }
+      }
+      // ---- O += P.V
+      const uint32_t vt = st + C::kTile;
+#pragma unroll
+      for (int kg = 0; kg < KS / 16; ++kg) {
+        const int k0 = kg * 16;
+        if constexpr (F16) {
+          constexpr int W = D / 32;  // words of a lane's run of a row
+          uint32_t w[4][W];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = k0 + 2 * c + (x & 1) + (x >> 1) * 8;
+            if constexpr (D == 128) {
+              const uint4 y = lds16(vt + v_off<KV, D>(key, quad));
+              w[x][0] = y.x; w[x][1] = y.y; w[x][W - 2] = y.z; w[x][W - 1] = y.w;
+            } else {
+              const uint2 y = lds8(vt + v_off<KV, D>(key, quad >> 1) + (quad & 1) * 8);
+              w[x][0] = y.x; w[x][1] = y.y;
             }
+          }
 #pragma unroll
-          for (int ss = 0; ss < D / 16; ++ss) {
-            uint32_t q4[MT][4];
-            if constexpr (C::kQSmem) {
+          for (int i = 0; i < W; ++i) {
+            uint32_t b0[4], b1[4];
+            codes4<KV>(__byte_perm(w[0][i], w[1][i], 0x5140), b0[0], b0[1]);
+            codes4<KV>(__byte_perm(w[0][i], w[1][i], 0x7362), b0[2], b0[3]);
+            codes4<KV>(__byte_perm(w[2][i], w[3][i], 0x5140), b1[0], b1[1]);
+            codes4<KV>(__byte_perm(w[2][i], w[3][i], 0x7362), b1[2], b1[3]);
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                const uint4 x = lds16(smem_u32(smem) + C::oQ + ((m * (D / 16) + ss) * 32 + lane) * 16);
-                q4[m][0] = x.x; q4[m][1] = x.y; q4[m][2] = x.z; q4[m][3] = x.w;
-              }
-            }
-#pragma unroll
-            for (int n = 0; n < SB / 8; ++n) {
-              uint32_t b0, b1;
-              codes4<KV>(w[n][ss], b0, b1);
-#pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                if constexpr (C::kQSmem) mma<F16>(s[m][n], q4[m], b0, b1);
-                else mma<F16>(s[m][n], qf[ss], b0, b1);
-              }
-            }
+            for (int y = 0; y < 4; ++y) mma<F16>(o[4 * i + y], pf[kg], b0[y], b1[y]);
           }
         } else {
 #pragma unroll
-          for (int sp = 0; sp < D / 32; ++sp) {
-            uint32_t q4[MT][2][4];
-            if constexpr (MT > 1) {
-#pragma unroll
-              for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int x2 = 0; x2 < 2; ++x2) {
-                  const uint4 x = lds16(smem_u32(smem) + C::oQ + ((m * (D / 16) + 2 * sp + x2) * 32 + lane) * 16);
-                  q4[m][x2][0] = x.x; q4[m][x2][1] = x.y; q4[m][x2][2] = x.z; q4[m][x2][3] = x.w;
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < SB / 8; ++n) {
-              uint32_t r[4];
-              ldsm4(st + k_off<KV, D>(sb + n * 8 + (lane & 7), 4 * sp + (lane >> 3)), r);
-#pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                if constexpr (MT > 1) {
-                  mma<F16>(s[m][n], q4[m][0], r[0], r[1]);
-                  mma<F16>(s[m][n], q4[m][1], r[2], r[3]);
-                } else {
-                  mma<F16>(s[m][n], qf[2 * sp], r[0], r[1]);
-                  mma<F16>(s[m][n], qf[2 * sp + 1], r[2], r[3]);
-                }
-              }
-            }
-          }
-        }
-        // ---- scores in log2 units, running max, P
-        uint32_t pf[MT][SB / 16][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          float iv[F16 ? SB / 8 : 1][2];
-          float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int n = 0; n < SB / 8; ++n) {
-            const int kk = sb + n * 8 + 2 * c;
-            float ks2[2] = {1.f, 1.f}, lv2[2] = {0.f, 0.f};
-            if constexpr (F16) {
-              const float2 x = *reinterpret_cast<const float2*>(sc + kk);
-              const float2 y = *reinterpret_cast<const float2*>(sc + 2 * KS + kk);
-              const float2 z = *reinterpret_cast<const float2*>(sc + 3 * KS + kk);
-              ks2[0] = x.x; ks2[1] = x.y; lv2[0] = y.x; lv2[1] = y.y;
-              iv[n][0] = z.x; iv[n][1] = z.y;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int e = k >> 1, j = t0 + kk + (k & 1);
-              float x;
-              if constexpr (MOD) {
-                float y = s[m][n][k] * xscale[m][e] * ks2[k & 1];
-                if (p.softcap > 0.f)  // c tanh(y / c) = c - 2 c / (1 + e^(2 y / c))
-                  y = fmaf(-2.f * p.softcap, rcp_approx(1.f + ex2_approx(y * icap2)), p.softcap);
-                y = fmaf(slope[m][e], (float)(j - pos[m][e]), y);
-                x = fmaf(y, kLog2e, lv2[k & 1]);
-              } else if constexpr (F16) {
-                x = fmaf(s[m][n][k] * ks2[k & 1], xscale[m][e] * kLog2e, lv2[k & 1]);
-              } else {
-                x = s[m][n][k] * (xscale[m][e] * kLog2e);
-              }
-              s[m][n][k] = x;
-            }
-          }
-          if (edge) {
-#pragma unroll
-            for (int n = 0; n < SB / 8; ++n)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int j = t0 + sb + n * 8 + 2 * c + (k & 1);
-                if (j > pos[m][k >> 1] || (p.window > 0 && j <= pos[m][k >> 1] - p.window)) s[m][n][k] = -INFINITY;
-              }
-          }
-#pragma unroll
-          for (int n = 0; n < SB / 8; ++n)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) top[k >> 1] = fmaxf(top[k >> 1], s[m][n][k]);
-          bool grow = false;
-          float al[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-            al[e] = 1.f;
-            if (top[e] > mx[m][e] + kLag<F16>) {  // from -inf too; false while both are
-              al[e] = ex2_approx(mx[m][e] - top[e]);
-              mx[m][e] = top[e];
-              grow = true;
-            }
-          }
-          if (__any_sync(0xffffffffu, grow)) {
-            l[m][0] *= al[0];
-            l[m][1] *= al[1];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              o[m][i][0] *= al[0]; o[m][i][1] *= al[0];
-              o[m][i][2] *= al[1]; o[m][i][3] *= al[1];
-            }
-          }
-          const float ms[2] = {mx[m][0] == -INFINITY ? 0.f : mx[m][0] - kShift,
-                               mx[m][1] == -INFINITY ? 0.f : mx[m][1] - kShift};
-#pragma unroll
-          for (int n = 0; n < SB / 8; ++n) {
-            float w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              w[k] = ex2_approx(s[m][n][k] - ms[k >> 1]);
-              if constexpr (F16) l[m][k >> 1] = fmaf(w[k], iv[n][k & 1], l[m][k >> 1]);
-              else l[m][k >> 1] += w[k];
-            }
-            uint32_t a0, a1;
-            if constexpr (F16) {
-              const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
-              memcpy(&a0, &h0, 4);
-              memcpy(&a1, &h1, 4);
-            } else {
-              a0 = pack_bf16x2(w[0], w[1]);
-              a1 = pack_bf16x2(w[2], w[3]);
-            }
-            pf[m][n >> 1][(n & 1) * 2] = a0;
-            pf[m][n >> 1][(n & 1) * 2 + 1] = a1;
-          }
-        }
-        // ---- O += P.V
-#pragma unroll
-        for (int kg = 0; kg < SB / 16; ++kg) {
-          const int k0 = sb + kg * 16;
-          const uint32_t vt = st + C::kTile;
-          if constexpr (F16) {
-            constexpr int W = D / 32;  // words of a lane's run of a row
-            uint32_t w[4][W];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int key = k0 + 2 * c + (x & 1) + (x >> 1) * 8;
-              if constexpr (D == 128) {
-                const uint4 y = lds16(vt + v_off<KV, D>(key, quad));
-                w[x][0] = y.x; w[x][1] = y.y; w[x][W - 2] = y.z; w[x][W - 1] = y.w;
-              } else {
-                const uint2 y = lds8(vt + v_off<KV, D>(key, quad >> 1) + (quad & 1) * 8);
-                w[x][0] = y.x; w[x][1] = y.y;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-              uint32_t b0[4], b1[4];
-              codes4<KV>(__byte_perm(w[0][i], w[1][i], 0x5140), b0[0], b0[1]);
-              codes4<KV>(__byte_perm(w[0][i], w[1][i], 0x7362), b0[2], b0[3]);
-              codes4<KV>(__byte_perm(w[2][i], w[3][i], 0x5140), b1[0], b1[1]);
-              codes4<KV>(__byte_perm(w[2][i], w[3][i], 0x7362), b1[2], b1[3]);
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-#pragma unroll
-                for (int m = 0; m < MT; ++m) mma<F16>(o[m][4 * i + y], pf[m][kg], b0[y], b1[y]);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              uint32_t r[4];
-              ldsm4t(vt + v_off<KV, D>(k0 + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * i + (lane >> 4)), r);
-#pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                mma<F16>(o[m][2 * i], pf[m][kg], r[0], r[1]);
-                mma<F16>(o[m][2 * i + 1], pf[m][kg], r[2], r[3]);
-              }
-            }
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t r[4];
+            ldsm4t(vt + v_off<KV, D>(k0 + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * i + (lane >> 4)), r);
+            mma<F16>(o[2 * i], pf[kg], r[0], r[1]);
+            mma<F16>(o[2 * i + 1], pf[kg], r[2], r[3]);
           }
         }
       }
     }
     cp_wait<0>();
 
-    // ---- the warps' parts into one
+    // ---- the streams' parts into one
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[m][e] += __shfl_xor_sync(0xffffffffu, l[m][e], 1);
-        l[m][e] += __shfl_xor_sync(0xffffffffu, l[m][e], 2);
-        if (c == 0) s_ml[warp * C::kRows + m * 16 + e * 8 + quad] = make_float2(mx[m][e], l[m][e]);
-      }
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (c == 0) s_ml[stream * C::kRows + rt * 16 + e * 8 + quad] = make_float2(mx[e], l[e]);
+    }
     __syncthreads();  // every ring is drained: its space holds the parts now
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int e = 0; e < 2; ++e) {
+      const int r = rt * 16 + e * 8 + quad;
+      float top = -INFINITY;
+      for (int w = 0; w < C::kStreams; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
+      const float f = mx[e] == -INFINITY ? 0.f : ex2_approx(mx[e] - top);
+      float* dst = mrg + (stream * C::kRows + r) * C::kPitch;
+      if (r < u.rows) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = m * 16 + e * 8 + quad;
-        float top = -INFINITY;
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
-        const float f = mx[m][e] == -INFINITY ? 0.f : ex2_approx(mx[m][e] - top);
-        float* dst = mrg + (warp * C::kRows + r) * C::kPitch;
-        if (r < u.rows) {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            if constexpr (F16) {
-              dst[(D / 8) * (2 * c) + i] = o[m][i][2 * e] * f;
-              dst[(D / 8) * (2 * c + 1) + i] = o[m][i][2 * e + 1] * f;
-            } else {
-              *reinterpret_cast<float2*>(dst + 8 * i + 2 * c) = make_float2(o[m][i][2 * e] * f, o[m][i][2 * e + 1] * f);
-            }
+        for (int i = 0; i < D / 8; ++i) {
+          if constexpr (F16) {
+            dst[(D / 8) * (2 * c) + i] = o[i][2 * e] * f;
+            dst[(D / 8) * (2 * c + 1) + i] = o[i][2 * e + 1] * f;
+          } else {
+            *reinterpret_cast<float2*>(dst + 8 * i + 2 * c) = make_float2(o[i][2 * e] * f, o[i][2 * e + 1] * f);
           }
         }
       }
+    }
     __syncthreads();
     const bool complete = ntile == u.nt;
     const long long slot = 2LL * blockIdx.x + (cur == begin ? 0 : 1);
-    if (!a.whole && tile0 == 0 && tid == 0) a.ws_first[(long long)b * p.c.Hkv + hk] = cur;
+    if (!a.whole && tile0 == 0 && tid == 0)
+      a.ws_unit[(long long)b * p.c.Hkv + hk] =
+          make_int4(blockIdx.x, owner(cur + u.nt - 1, T, work_ctas), cur == begin ? 0 : 1, 0);
     for (int i = tid; i < u.rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
       float top = -INFINITY, den = 0.f;
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
+      for (int w = 0; w < C::kStreams; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < C::kStreams; ++w) {
         const float2 ml = s_ml[w * C::kRows + r];
         if (ml.x != -INFINITY) den = fmaf(ex2_approx(ml.x - top), ml.y, den);
         const float4 y = *reinterpret_cast<const float4*>(mrg + (w * C::kRows + r) * C::kPitch + x);
@@ -723,7 +671,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
   for (int unit = blockIdx.x; unit < p.s.B * p.c.Hkv; unit += G) {
     const int bb = unit / p.c.Hkv, hk = unit - bb * p.c.Hkv;
     const Unit u = unit_of<C::kKeys>(a, bb);
-    if (u.nt != 0 || u.rows == 0 || u.rows > a.limit) continue;
+    if (u.nt != 0) continue;
+    if (!a.whole && tid == 0) a.ws_unit[unit] = make_int4(0, 0, 0, 0);
+    if (u.rows == 0 || u.rows > a.limit) continue;
     for (int i = tid; i < u.rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
       const int tok = r / p.group, h = hk * p.group + r - tok * p.group;
@@ -735,46 +685,58 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
 }
 
 // Adds the parts of every unit that several CTAs share: O = sum 2^(m_i - M) O_i
-// over sum 2^(m_i - M) l_i, in the order of the tiles.  One block per unit.
-template <int TK, int D, int ROWS>
+// over sum 2^(m_i - M) l_i, in the order of the tiles.  One block per unit; a
+// part's (m, l) and O are loaded together, and the running max of a few parts at
+// a time keeps their loads apart from one another.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) paged_merge_kernel(const __grid_constant__ DecodeArgs a, float shift) {
   const PagedParams& p = a.p;
   const int b = blockIdx.x / p.c.Hkv, hk = blockIdx.x - b * p.c.Hkv;
   grid_dep_wait();
   grid_dep_launch();
-  const Unit u = unit_of<TK>(a, b);
-  if (u.nt == 0) return;
-  const long long T = a.ws_hdr[0];
-  const int G = (int)a.ws_hdr[1];
-  const long long f = a.ws_first[blockIdx.x];
-  const int c0 = owner(f, T, G), c1 = owner(f + u.nt - 1, T, G);
+  const int4 w = a.ws_unit[blockIdx.x];
+  const Seq s = seq_of(p.s, p.c, b, p.err);
+  const int c0 = w.x, c1 = w.y;
   if (c0 == c1) return;
-  const long long first0 = div64(T * c0, G);  // c0's first tile
-  for (int i = threadIdx.x; i < u.rows * (D / 4); i += kThreads) {
+  for (int i = threadIdx.x; i < s.n * p.group * (D / 4); i += kThreads) {
     const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
-    auto slot = [&](int cta) { return 2LL * cta + (cta == c0 && f > first0 ? 1 : 0); };
     float top = -INFINITY, den = 0.f;
-    for (int q = c0; q <= c1; ++q) top = fmaxf(top, a.ws_ml[slot(q) * ROWS + r].x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int q = c0; q <= c1; ++q) {
-      const long long s = slot(q) * ROWS + r;
-      const float2 ml = a.ws_ml[s];
-      const float4 y = *reinterpret_cast<const float4*>(a.ws_o + s * D + x);
-      const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
-      den = fmaf(w, ml.y, den);
-      acc.x = fmaf(w, y.x, acc.x); acc.y = fmaf(w, y.y, acc.y);
-      acc.z = fmaf(w, y.z, acc.z); acc.w = fmaf(w, y.w, acc.w);
+    constexpr int kAtOnce = 6;
+    for (int q0 = c0; q0 <= c1; q0 += kAtOnce) {
+      float2 ml[kAtOnce];
+      float4 y[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const long long at = (2LL * min(q0 + k, c1) + (q0 + k == c0 ? w.z : 0)) * ROWS + r;
+        ml[k] = a.ws_ml[at];
+        y[k] = *reinterpret_cast<const float4*>(a.ws_o + at * D + x);
+        if (q0 + k > c1) ml[k].x = -INFINITY;
+      }
+      float m = top;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) m = fmaxf(m, ml[k].x);
+      const float old = top == -INFINITY ? 0.f : ex2_approx(top - m);
+      top = m;
+      den *= old;
+      acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float f = ml[k].x == -INFINITY ? 0.f : ex2_approx(ml[k].x - m);
+        den = fmaf(f, ml[k].x == -INFINITY ? 0.f : ml[k].y, den);
+        acc.x = fmaf(f, y[k].x, acc.x); acc.y = fmaf(f, y[k].y, acc.y);
+        acc.z = fmaf(f, y[k].z, acc.z); acc.w = fmaf(f, y[k].w, acc.w);
+      }
     }
     const int tok = r / p.group, h = hk * p.group + r - tok * p.group;
     const float inv = den > 0.f ? 1.f / den : 0.f;
     uint2 y;
     y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
     y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (long long)(u.s.q0 + tok) * p.ot + (long long)h * p.oh;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (long long)(s.q0 + tok) * p.ot + (long long)h * p.oh;
     *reinterpret_cast<uint2*>(dst + x) = y;
     if (x == 0 && p.lse)
-      p.lse[(long long)(u.s.q0 + tok) * p.Hq + h] = den > 0.f ? (top - shift) * kLn2 + logf(den) : -INFINITY;
+      p.lse[(long long)(s.q0 + tok) * p.Hq + h] = den > 0.f ? (top - shift) * kLn2 + logf(den) : -INFINITY;
   }
 }
 
@@ -800,7 +762,7 @@ cudaError_t decode_one(DecodeArgs& a, bool mod, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_serialized(kern, dim3((unsigned)ctas), dim3(kThreads), (size_t)C::kTotal, stream, a);
   if (e != cudaSuccess || a.whole) return e;
-  return launch_serialized(paged_merge_kernel<C::kKeys, D, C::kRows>, dim3((unsigned)(a.p.s.B * a.p.c.Hkv)),
+  return launch_serialized(paged_merge_kernel<D, C::kRows>, dim3((unsigned)(a.p.s.B * a.p.c.Hkv)),
                            dim3(kThreads), 0, stream, a, kOffset<KV != KV_BF16>);
 }
 template <int KV, int D>
@@ -818,7 +780,7 @@ bool whole_units(const PagedParams& p) { return (long long)p.s.max_pages * p.c.p
 
 // One resident wave.
 int decode_ctas(const PagedParams& p) {
-  return num_sms() * (p.c.dtype != SDPA_CACHE_BF16 && row_limit(p) == 16 ? 3 : 2);
+  return num_sms() * (p.c.dtype != SDPA_CACHE_BF16 ? 3 : 2);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -843,7 +805,7 @@ int paged_decode_check(const PagedParams& p, sdpa_dtype_t dtype) {
 size_t paged_decode_workspace(const PagedParams& p) {
   if (whole_units(p) || p.s.total_q == 0) return 0;
   const size_t slots = 2 * (size_t)decode_ctas(p), rows = row_limit(p);
-  return up256(slots * rows * p.c.d * 4) + up256(slots * rows * 8) + up256((size_t)p.s.B * p.c.Hkv * 8) + 256;
+  return up256(slots * rows * p.c.d * 4) + up256(slots * rows * 8) + up256((size_t)p.s.B * p.c.Hkv * 16);
 }
 
 cudaError_t launch_paged_decode(const PagedParams& p, void* ws, cudaStream_t stream) {
@@ -860,9 +822,7 @@ cudaError_t launch_paged_decode(const PagedParams& p, void* ws, cudaStream_t str
     w += up256(slots * rows * p.c.d * 4);
     a.ws_ml = reinterpret_cast<float2*>(w);
     w += up256(slots * rows * 8);
-    a.ws_first = reinterpret_cast<long long*>(w);
-    w += up256((size_t)p.s.B * p.c.Hkv * 8);
-    a.ws_hdr = reinterpret_cast<long long*>(w);
+    a.ws_unit = reinterpret_cast<int4*>(w);
   }
   const bool mod = p.softcap > 0.f || p.slopes != nullptr;
   const bool wide = p.c.d == 128;
