@@ -229,14 +229,14 @@ extern "C" int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const
   const int rc = build_paged(q, q_strides, cache, batch, out, out_strides, dtype, Hq, scale, window, softcap, slopes, lse, &p);
   if (rc != SDPA_OK) return rc;
   if (p.s.total_q == 0) return SDPA_OK;
-  p.err = error_word();
-  if (p.err == nullptr) return SDPA_ERR_CUDA;
   const Plan plan = make_plan(p, dtype, path);
   if (plan.status != SDPA_OK) return plan.status;
   if (plan.ws_bytes > 0) {
     if (workspace == nullptr || workspace_bytes < plan.ws_bytes) return SDPA_ERR_CAPACITY;
     if (!aligned_to(workspace, 16)) return SDPA_ERR_MISALIGNED;
   }
+  p.err = error_word();
+  if (p.err == nullptr) return SDPA_ERR_CUDA;
   if (plan.decode && launch_paged_decode(p, workspace, stream) != cudaSuccess) return SDPA_ERR_CUDA;
   if (plan.tc && launch_paged_tc(p, plan.limit, static_cast<char*>(workspace) + plan.decode_ws, stream) != cudaSuccess)
     return SDPA_ERR_CUDA;

@@ -265,3 +265,253 @@ def test_chunk_more_rows_than_tokens(cdt):
 def test_auto_mixed(d, cdt):
     """Single tokens, drafts and chunks of one batch: two kernels share it."""
     run_case("auto", cdt, BF16, 8, 2, d, 16, [700, 65, 0, 300, 128, 1000], [1, 5, 0, 120, 128, 9], seed=7)
+
+
+# ------------------------------------------------------------------ what the kernels check
+def bad_batch(path, *, table=None, lens=None, cuq=None, max_q=2):
+    pool = R.Pool(BF16, 2, 64, 16, [100, 60], seed=2, garbage=False)
+    q = torch.randn(4, 8, 64, device="cuda").to(BF16)
+    t, l, c = pool.table.clone(), pool.lens.clone(), torch.tensor([0, 2, 4], dtype=torch.int32)
+    for x, change in ((t, table), (l, lens), (c, cuq)):
+        for at, v in (change or {}).items():
+            x[at] = v
+    S.sdpa_paged(q, pool.cache(), t.cuda(), l.cuda(), c.cuda(), max_q=max_q, path=path)
+    return device_error()
+
+
+@pytest.mark.parametrize("path", ["exact", "decode", "tcgen05"])
+@pytest.mark.parametrize("kw", [dict(table={(0, 1): 10 ** 6}), dict(table={(1, 3): -5}), dict(lens={0: -1}),
+                                dict(lens={1: 10 ** 9}), dict(cuq={1: 5}), dict(cuq={1: -1}), dict(cuq={2: 1}),
+                                dict(cuq={2: 400}), dict(max_q=1)], ids=str)
+def test_bad_device_values_are_reported(path, kw):
+    """Pages, lengths and ranges only the kernels see: an error word, nothing else."""
+    assert bad_batch(path) == 0
+    assert bad_batch(path, **kw) == -7
+    assert bad_batch(path) == 0
+
+
+def test_entries_past_the_tokens_are_not_read():
+    """Table entries behind a sequence's tokens, and in front of its window, may be anything."""
+    for path in ("exact", "decode", "tcgen05"):
+        for cdt in (BF16, E4M3):
+            pool = R.Pool(cdt, 2, 64, 16, [1000], seed=4)
+            q = torch.randn(3, 4, 64, generator=torch.Generator().manual_seed(1)).to(BF16)
+            a = S.sdpa_paged(q.cuda(), pool.cache(), pool.table.cuda(), pool.lens.cuda(), cu([3]), max_q=3, window=50, path=path)
+            t = torch.full((1, 90), -7, dtype=torch.int32)
+            first = (1000 - 3 + 1 - 50) // 16
+            t[0, first:63] = pool.table[0, first:63]
+            b = S.sdpa_paged(q.cuda(), pool.cache(), t.cuda(), pool.lens.cuda(), cu([3]), max_q=3, window=50, path=path)
+            assert device_error() == 0
+            u_p = 0.0 if path == "exact" else R.U[torch.float16 if cdt == E4M3 else BF16]
+            want, _, tol, _ = R.attend(pool, q, [3], window=50, u_p=u_p, p_floor=2.0 ** -37 if cdt == E4M3 else 0.0,
+                                       u_kv=2.0 ** -11 if cdt == E4M3 else 0.0)
+            R.check(a, want, tol, BF16, f"{path} {cdt}")
+            R.check(b, want, tol, BF16, f"{path} {cdt} with freed pages")
+
+
+def test_bad_write_and_read_are_reported():
+    pool = R.Pool(E4M3, 2, 64, 16, [100, 60], seed=2, garbage=False)
+    x = torch.randn(4, 2, 64, device="cuda").to(BF16)
+    for change in (lambda t, l, c: t.__setitem__((0, 6), 99), lambda t, l, c: l.__setitem__(1, 1),
+                   lambda t, l, c: l.__setitem__(0, 10 ** 6), lambda t, l, c: c.__setitem__(2, 9)):
+        t, l, c = pool.table.clone(), pool.lens.clone(), torch.tensor([0, 2, 4], dtype=torch.int32)
+        change(t, l, c)
+        S.cache_write(pool.cache(), x, x, t.cuda(), l.cuda(), c.cuda(), max_q=2)
+        assert device_error() == -7
+    t = pool.table.clone()
+    t[0, 2] = -1
+    S.cache_read(pool.cache(), t.cuda(), pool.lens.cuda(), T=100)
+    assert device_error() == -7
+
+
+# ------------------------------------------------------------------ together, as they are used
+@pytest.mark.parametrize("cdt", [BF16, E4M3, INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_then_decode_equals_dense(d, cdt):
+    """A prompt written in two chunks, then token by token, attended at each
+    step, against dense causal attention (``sdpa``) of what the cache holds,
+    read back; 8-bit caches and the dense call round keys, values and weights
+    each their own way: 2^-8 for every bf16 rounding there is."""
+    Hq, Hkv, page, n = 8, 2, 16, [150, 61]
+    g = torch.Generator().manual_seed(3)
+    total = [x + 5 for x in n]
+    k, v, q = (torch.randn(2, max(total), h, d, generator=g).to(BF16).cuda() for h in (Hkv, Hkv, Hq))
+    cache = S.KVCache.empty(40, page, Hkv, d, cdt)
+    table = torch.randperm(40, generator=g).int()[:24].view(2, 12).cuda()
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    got = torch.zeros(2, max(total), Hq, d, dtype=BF16, device="cuda")
+    done = [0, 0]
+    steps = [[100, 20], [50, 41]] + [[1, 1]] * 5
+    for step in steps:
+        rows = [slice(a, a + m) for a, m in zip(done, step)]
+        cat = lambda t: torch.cat([t[b, r] for b, r in enumerate(rows)])
+        lens += torch.tensor(step, dtype=torch.int32, device="cuda")
+        single = step == [1, 1]
+        args = (table, lens, None if single else cu(step))
+        S.cache_write(cache, cat(k), cat(v), *args, max_q=max(step))
+        out = S.sdpa_paged(cat(q), cache, *args, max_q=max(step))
+        at = 0
+        for b, (r, m) in enumerate(zip(rows, step)):
+            got[b, r] = out[at:at + m]
+            at += m
+            done[b] += m
+    kd, vd = S.cache_read(cache, table, lens, T=max(total))
+    want = S.sdpa(q.transpose(1, 2), kd, vd, mask_kind=S.MASK_CAUSAL).transpose(1, 2)
+    assert device_error() == 0
+    size = S.sdpa(q.transpose(1, 2), kd, vd.abs(), mask_kind=S.MASK_CAUSAL).transpose(1, 2).float()
+    for b in range(2):
+        a, w, z = got[b, :total[b]].float(), want[b, :total[b]].float(), size[b, :total[b]]
+        # two outputs rounded (|w|, |a|), P rounded twice, K (its score error bounded by 2^-8 of sum |q k| scale,
+        # below 8 for these sizes) and V rounded by the read, size itself off by two roundings
+        tol = 2.0 ** -8 * (2 * w.abs() + (3 + 2 * 8 * (cdt != BF16)) * z) * 1.02
+        assert ((a - w).abs() <= tol + 1e-6).all()
+
+
+def test_f32_chain():
+    pool_kv = [0, 0]
+    cache = S.KVCache.empty(8, 8, 2, 16, F32)
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    g = torch.Generator().manual_seed(1)
+    k, v, q = (torch.randn(2, 20, h, 16, generator=g).cuda() for h in (2, 2, 4))
+    lens = torch.tensor([20, 13], dtype=torch.int32, device="cuda")
+    cat = lambda t: torch.cat([t[0], t[1, :13]])
+    S.cache_write(cache, cat(k), cat(v), table, lens, cu([20, 13]))
+    out = S.sdpa_paged(cat(q), cache, table, lens, cu([20, 13]))
+    kd, vd = S.cache_read(cache, table, lens, T=20)
+    want = S.sdpa(q.transpose(1, 2), kd, vd, mask_kind=S.MASK_CAUSAL).transpose(1, 2)
+    assert device_error() == 0 and pool_kv == [0, 0]
+    assert torch.equal(kd[0].transpose(0, 1), k[0]) and (kd[1, :, 13:] == 0).all()
+    assert (out[:20] - want[0]).abs().max() < 1e-4 and (out[20:] - want[1, :13]).abs().max() < 1e-4
+
+
+def decode_setup(cdt=BF16, d=64, kv=(700, 300, 64)):
+    pool = R.Pool(cdt, 2, d, 16, list(kv), seed=6, garbage=False)
+    q = torch.randn(len(kv), 8, d, generator=torch.Generator().manual_seed(2)).to(BF16).cuda()
+    k, v = (torch.randn(len(kv), 2, d, generator=torch.Generator().manual_seed(3 + i)).to(BF16).cuda() for i in range(2))
+    return pool, q, k, v, pool.table.cuda(), pool.lens.cuda()
+
+
+@pytest.mark.parametrize("cdt", [BF16, E4M3])
+def test_graph_replays_with_new_lengths(cdt):
+    """A captured step replays with what lengths, tables and rows hold then."""
+    pool, q, k, v, table, lens = decode_setup(cdt)
+    cache = pool.cache()
+    step = lambda: S.sdpa_paged(q, S.cache_write(cache, k, v, table, lens), table, lens)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for new in ([5, 300, 1], [700, 64, 17], [699, 0, 64]):
+        lens.copy_(torch.tensor(new, dtype=torch.int32))
+        if 0 in new:
+            lens[1] = 16
+        q.normal_()
+        k.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, step()) and device_error() == 0
+
+
+def test_two_graphs_and_two_streams_do_not_share_scratch():
+    """Calls whose kernels overlap keep to their own workspaces: two captured
+    graphs and eager calls on two streams at once."""
+    sets = [decode_setup(BF16, 64, kv) for kv in ((4000, 900, 64), (3000, 2500, 1))]
+    caches = [s[0].cache() for s in sets]
+    plain = [S.sdpa_paged(s[1], c, s[4], s[5]).clone() for s, c in zip(sets, caches)]
+    chunk = [torch.randn(200, 8, 64, device="cuda").to(BF16) for _ in range(2)]
+    cuq = [cu([100, 50, 50]), cu([180, 20, 0])]
+    plain2 = [S.sdpa_paged(x, c, s[4], s[5], u, max_q=180).clone() for x, c, s, u in zip(chunk, caches, sets, cuq)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((S.sdpa_paged(sets[i][1], caches[i], sets[i][4], sets[i][5]),
+                         S.sdpa_paged(chunk[i], caches[i], sets[i][4], sets[i][5], cuq[i], max_q=180)))
+        graphs.append(g)
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    eager = []
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                eager.append((i, S.sdpa_paged(sets[i][1], caches[i], sets[i][4], sets[i][5])))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i][0], plain[i]) and torch.equal(outs[i][1], plain2[i])
+    for i, o in eager:
+        assert torch.equal(o, plain[i])
+    assert device_error() == 0
+
+
+def test_stream_argument():
+    pool, q, k, v, table, lens = decode_setup(E4M3)
+    cache = pool.cache()
+    want = S.sdpa_paged(q, cache, table, lens)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    busy = torch.zeros(1 << 26, device="cuda")
+    with torch.cuda.stream(st):
+        busy.add_(1)
+    got = S.sdpa_paged(q, cache, table, lens, stream=st)
+    S.cache_read(cache, table, lens, T=10, stream=st)
+    st.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_strided_rows_and_padding_rows():
+    """q and out as slices of wider tensors, rows behind the last sequence kept."""
+    for path, cdt in itertools.product(("exact", "auto", "tcgen05"), (BF16, INT8)):
+        pool = R.Pool(cdt, 2, 64, 32, [70, 200], seed=8)
+        n = [3, 90]
+        wide = torch.randn(100, 8 + 4, 64, generator=torch.Generator().manual_seed(1)).to(BF16).cuda()
+        q, out = wide[:, :8], torch.full((100, 10, 64), 7.0, dtype=BF16, device="cuda")
+        S.sdpa_paged(q, pool.cache(), pool.table.cuda(), pool.lens.cuda(), cu(n), max_q=90, out=out[:, 1:9], path=path)
+        assert device_error() == 0
+        codes = cdt == INT8
+        u_p = 0.0 if path == "exact" else R.U[torch.float16 if codes else BF16]
+        want, _, tol, _ = R.attend(pool, q[:93].cpu(), n, u_p=u_p, p_floor=2.0 ** -37 if codes else 0.0,
+                                   u_kv=2.0 ** -11 if codes else 0.0)
+        R.check(out[:93, 1:9], want, tol, BF16, f"{path} {cdt}")
+        assert (out[93:] == 7).all() and (out[:, 0] == 7).all() and (out[:, 9] == 7).all()
+
+
+@pytest.mark.parametrize("cdt", [BF16, E4M3])
+def test_auto_takes_odd_layouts(cdt):
+    """A page size and strides that only the exact kernel takes."""
+    run_case("auto", cdt, BF16, 8, 2, 64, 20, [100, 31], [40, 3])
+    pool = R.Pool(cdt, 2, 64, 16, [100], seed=5)
+    q = torch.randn(1, 8, 65, device="cuda").to(BF16)[:, :, :64]
+    out = S.sdpa_paged(q, pool.cache(), pool.table.cuda(), pool.lens.cuda())
+    want, _, tol, _ = R.attend(pool, q.cpu(), [1])
+    R.check(out, want, tol, BF16)
+
+
+def test_large_offsets():
+    """A pool whose last pages lie past 2^31 elements."""
+    pages, page, Hkv, d = 70000, 128, 2, 128
+    k = torch.zeros(pages, Hkv, page, d, dtype=torch.int8, device="cuda")
+    assert (pages - 1) * Hkv * page * d > 2 ** 31
+    cache = S.KVCache(k, torch.zeros_like(k), *(torch.ones(pages, Hkv, page, device="cuda") for _ in range(2)))
+    table = torch.tensor([[pages - 1, 3, pages - 2]], dtype=torch.int32, device="cuda")
+    kv, n = 300, 150
+    g = torch.Generator().manual_seed(1)
+    kn, vn = (torch.randn(kv, Hkv, d, generator=g).to(BF16).cuda() for _ in range(2))
+    lens = torch.tensor([kv], dtype=torch.int32, device="cuda")
+    S.cache_write(cache, kn, vn, table, lens, cu([kv]))
+    kd, vd = S.cache_read(cache, table, lens, T=kv)
+    c, s = R.quantise(kn.cpu(), INT8)
+    assert torch.equal(kd[0].transpose(0, 1).cpu(), (c * s[..., None]).to(BF16))
+    q = torch.randn(n, 8, d, generator=g).to(BF16).cuda()
+    outs = [S.sdpa_paged(q, cache, table, lens, cu([n]), path=p) for p in ("exact", "tcgen05")]
+    one = [S.sdpa_paged(q[-1:], cache, table, lens, path=p) for p in ("exact", "decode")]
+    assert device_error() == 0
+    # both within 2^-8 of rounding and (codes) 2^-11 of P, K and V of one another's sums
+    for a, b in (outs, one):
+        assert (a.float() - b.float()).abs().max() < 2.0 ** -5 and (a.float() - b.float()).abs().mean() < 2.0 ** -9
+    assert torch.isfinite(outs[0]).all()
