@@ -13,6 +13,7 @@
 // its amax is a few shuffles and nothing is staged; a warp keeps several rows
 // in flight to cover the latency of their loads.
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.cuh"
 #include "pdl_launch.cuh"
@@ -38,25 +39,75 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int t, int lane) {
   return lo;
 }
 
-template <typename T, typename C>
-__device__ __forceinline__ C encode(float x, float s);
-template <> __device__ __forceinline__ float encode<float, float>(float x, float) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 encode<__nv_bfloat16, __nv_bfloat16>(float x, float) {
-  return __float2bfloat16_rn(x);
+// fl(x / s) for the many x of a row, from r = fl(1 / s): q = fl(x r) is within
+// an ulp, and q + fl(x - q s) r, both fused, is the correctly rounded quotient
+// unless s's significand is all ones (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990).  Three operations
+// an element; a division each had taken the write of a long prompt from TODO.
+// r = 0 asks for the division: all-ones significands, and scales so large that
+// r or the remainder could leave the normal range.  (Small x can make the
+// remainder inexact only where the code is 0 either way: s >= 2^-30.)
+__device__ __forceinline__ float row_reciprocal(float s) {
+  const bool plain = s < 1e30f && (__float_as_uint(s) & 0x7fffffu) != 0x7fffffu;
+  return plain ? __frcp_rn(s) : 0.f;
 }
-__device__ __forceinline__ __nv_fp8_e4m3 to_e4m3(float x, float s) {
-  __nv_fp8_e4m3 r;
-  r.__x = __nv_cvt_float_to_fp8(__fdiv_rn(x, s), __NV_SATFINITE, __NV_E4M3);
-  return r;
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, s, x), r, q);
 }
-__device__ __forceinline__ int8_t to_int8(float x, float s) {
-  const float y = rintf(__fdiv_rn(x, s));
-  return (int8_t)(int)fminf(fmaxf(y != y ? 0.f : y, -127.f), 127.f);
+// y = fl(x / s) to the code.  |y| <= Q by the choice of s, so nothing saturates;
+// adding 1.5 2^23 leaves the integer nearest to y, ties to even, in the low bits.
+template <typename C>
+__device__ __forceinline__ uint32_t codes_of(float a, float b, float c, float d) {
+  if constexpr (std::is_same<C, int8_t>::value) {
+    auto low = [](float y) { return y == y ? __float_as_uint(y + 12582912.f) : 0u; };
+    return __byte_perm(__byte_perm(low(a), low(b), 0x0040), __byte_perm(low(c), low(d), 0x0040), 0x5410);
+  } else {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+  }
 }
-template <> __device__ __forceinline__ __nv_fp8_e4m3 encode<float, __nv_fp8_e4m3>(float x, float s) { return to_e4m3(x, s); }
-template <> __device__ __forceinline__ __nv_fp8_e4m3 encode<__nv_bfloat16, __nv_fp8_e4m3>(float x, float s) { return to_e4m3(x, s); }
-template <> __device__ __forceinline__ int8_t encode<float, int8_t>(float x, float s) { return to_int8(x, s); }
-template <> __device__ __forceinline__ int8_t encode<__nv_bfloat16, int8_t>(float x, float s) { return to_int8(x, s); }
+// The E elements of a 16-byte piece as fp32.
+__device__ __forceinline__ float piece_elem(const uint32_t (&w)[4], int n, float) { return __uint_as_float(w[n]); }
+__device__ __forceinline__ float piece_elem(const uint32_t (&w)[4], int n, __nv_bfloat16) {
+  return __uint_as_float(n & 1 ? w[n >> 1] & 0xffff0000u : w[n >> 1] << 16);
+}
+// Their largest magnitude; NaN elements are passed over.
+__device__ __forceinline__ float piece_amax(const uint32_t (&w)[4], float) {
+  float m = 0.f;
+#pragma unroll
+  for (int n = 0; n < 4; ++n) m = fmaxf(m, fabsf(__uint_as_float(w[n])));
+  return m;
+}
+__device__ __forceinline__ float piece_amax(const uint32_t (&w)[4], __nv_bfloat16) {
+  __nv_bfloat162 m = __float2bfloat162_rn(0.f), x;
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    memcpy(&x, &w[n], 4);
+    m = __hmax2(m, __habs2(x));
+  }
+  return fmaxf(__low2float(m), __high2float(m));
+}
+template <typename T, typename C, int E>
+__device__ __forceinline__ void encode_piece(const uint32_t (&w)[4], float s, uint32_t (&out)[E * sizeof(C) / 4]) {
+  if constexpr (is_code<C>::value) {
+    const float r = row_reciprocal(s);
+    float q[E];
+#pragma unroll
+    for (int n = 0; n < E; ++n) q[n] = quotient(piece_elem(w, n, T()), s, r);
+    if (r == 0.f) {
+#pragma unroll
+      for (int n = 0; n < E; ++n) q[n] = __fdiv_rn(piece_elem(w, n, T()), s);
+    }
+#pragma unroll
+    for (int n = 0; n < E; n += 4) out[n / 4] = codes_of<C>(q[n], q[n + 1], q[n + 2], q[n + 3]);
+  } else {
+    static_assert(std::is_same<T, C>::value, "copied as it is");
+#pragma unroll
+    for (int n = 0; n < 4; ++n) out[n] = w[n];
+  }
+}
 template <typename C> constexpr float code_max() { return std::is_same<C, int8_t>::value ? 127.f : 448.f; }
 
 struct WriteArgs {
@@ -65,21 +116,24 @@ struct WriteArgs {
   const void* k;
   const void* v;
   long long kt, kh, vt, vh;
-  int vec;  // sources and cache rows allow whole-piece accesses
-  int tb;   // tokens of a block
-  int ppt;  // 16-byte pieces of a token: 2 Hkv D / E
-  FastDiv fd_ppt;
+  int vec;   // sources and cache rows allow whole-piece accesses
+  int tb;    // tokens of a block
+  int ppt;   // 16-byte pieces of a token: 2 Hkv D / E
+  int per;   // pieces of a token a block's threads have at once, a multiple of a row's
+  int side;  // tokens side by side
+  FastDiv fd_per;
   int* err;
 };
 
-constexpr int kMaxTok = 8;  // tokens of a block at most
-constexpr int kAhead = 4;   // pieces a thread has in flight
+constexpr int kMaxTok = 32;  // tokens of a block at most
+constexpr int kAhead = 4;    // pieces a thread has in flight
 
 // T: elements given, C: elements kept.  A block takes tb tokens, all heads of k
-// and v; a thread 16 bytes of a row at a time.  While its first pieces are on
+// and v.  A thread keeps its place in a token (16 bytes of one row) and walks
+// the tokens, so rows and heads are divided once.  While its first pieces are on
 // their way one warp looks up where the tokens go.
 template <typename T, typename C, int D>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) cache_write_kernel(const __grid_constant__ WriteArgs a) {
   constexpr int E = 16 / sizeof(T);  // elements of a piece
   constexpr int G = D / E;           // pieces (neighbouring lanes) of a row
   __shared__ int s_page[kMaxTok], s_off[kMaxTok];
@@ -87,93 +141,98 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
   sm100::grid_dep_wait();
   const int tid = threadIdx.x, lane = tid & 31;
   const int t0 = blockIdx.x * a.tb;
-  const int pieces = min(a.tb, a.s.total_q - t0) * a.ppt;
-  for (int base = 0; base < pieces; base += kThreads * kAhead) {
-    float x[kAhead][E];
-    int tok[kAhead], row[kAhead];  // token of the block; row of the token: k heads, then v heads
+  const int ntok = min(a.tb, a.s.total_q - t0);
+  const int tl = (int)fdiv((uint32_t)tid, a.fd_per), pc = tid - tl * a.per;
+  bool looked_up = false;
+  for (int c = 0; c < a.ppt; c += a.per) {
+    const int row = (c + pc) / G;  // k heads, then v heads
+    const bool mine = tl < a.side && c + pc < a.ppt;
+    const bool is_v = row >= a.c.Hkv;
+    const int h = is_v ? row - a.c.Hkv : row;
+    const long long st = is_v ? a.vt : a.kt, dp = is_v ? a.c.vp : a.c.kp, dt = is_v ? a.c.vt : a.c.kt;
+    const T* src = static_cast<const T*>(is_v ? a.v : a.k) + h * (is_v ? a.vh : a.kh) + t0 * st + (tid % G) * E;
+    C* dst = static_cast<C*>(is_v ? a.c.v : a.c.k) + h * (is_v ? a.c.vh : a.c.kh) + (tid % G) * E;
+    for (int base = 0; base < ntok; base += a.side * kAhead) {
+      uint32_t x[kAhead][4];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int i = base + u * kThreads + tid;
-      tok[u] = -1;
-      if (i < pieces) {
-        tok[u] = (int)fdiv((uint32_t)i, a.fd_ppt);
-        row[u] = (i - tok[u] * a.ppt) / G;
-        const bool is_v = row[u] >= a.c.Hkv;
-        const int h = is_v ? row[u] - a.c.Hkv : row[u];
-        const long long t = t0 + tok[u];
-        const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (is_v ? t * a.vt + h * a.vh : t * a.kt + h * a.kh) +
-                       (tid % G) * E;
-        if (a.vec) {
-          const uint4 raw = __ldg(reinterpret_cast<const uint4*>(src));
-          const T* e = reinterpret_cast<const T*>(&raw);
+      for (int u = 0; u < kAhead; ++u) {
+        const int t = base + u * a.side + tl;
+        if (mine && t < ntok) {
+          const T* at = src + t * st;
+          if (a.vec) {
+            const uint4 raw = __ldg(reinterpret_cast<const uint4*>(at));
+            x[u][0] = raw.x; x[u][1] = raw.y; x[u][2] = raw.z; x[u][3] = raw.w;
+          } else {
+            alignas(16) T e[E];
 #pragma unroll
-          for (int n = 0; n < E; ++n) x[u][n] = to_f32(e[n]);
-        } else {
-#pragma unroll
-          for (int n = 0; n < E; ++n) x[u][n] = to_f32(src[n]);
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < E; ++n) x[u][n] = 0.f;
-      }
-    }
-    if (base == 0) {
-      if (tid < 32) {
-        const int first = a.s.cu_q ? find_seq(a.s.cu_q, a.s.B, t0, lane) : 0;
-        if (lane < a.tb && t0 + lane < a.s.total_q) {
-          const int t = t0 + lane;
-          int b = t, page = -1, off = 0;
-          if (a.s.cu_q)
-            for (b = first; b + 1 < a.s.B && __ldg(a.s.cu_q + b + 1) <= t;) ++b;
-          const Seq q = seq_of(a.s, a.c, b, a.err);
-          // rows behind the last sequence and rows without a place are left out
-          if (t >= q.q0 && t < q.q0 + q.n) {
-            const int pos = q.L - q.n + (t - q.q0);
-            if (pos < 0) {
-              index_error(a.err);
-            } else {
-              page = page_or_bad(a.s, a.c, b, pos, a.err);
-              off = pos - (int)fdiv((uint32_t)pos, a.c.fd_page) * a.c.page_size;
-            }
+            for (int n = 0; n < E; ++n) e[n] = at[n];
+            memcpy(x[u], e, 16);
           }
-          s_page[lane] = page;
-          s_off[lane] = off;
+        } else {
+          x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0;
         }
       }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      float s = 1.f;
-      if (is_code<C>::value) {
-        float m = 0.f;
-#pragma unroll
-        for (int n = 0; n < E; ++n) m = fmaxf(m, fabsf(x[u][n]));
-#pragma unroll
-        for (int o = 1; o < G; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        s = fmaxf(__fdiv_rn(m, code_max<C>()), kScaleFloor);
+      if (!looked_up) {
+        looked_up = true;
+        if (tid < 32) {
+          const int first = a.s.cu_q ? find_seq(a.s.cu_q, a.s.B, t0, lane) : 0;
+          if (lane < ntok) {
+            const int t = t0 + lane;
+            int b = t, page = -1, off = 0;
+            if (a.s.cu_q)
+              for (b = first; b + 1 < a.s.B && __ldg(a.s.cu_q + b + 1) <= t;) ++b;
+            const Seq q = seq_of(a.s, a.c, b, a.err);
+            // rows behind the last sequence and rows without a place are left out
+            if (t >= q.q0 && t < q.q0 + q.n) {
+              const int pos = q.L - q.n + (t - q.q0);
+              if (pos < 0) {
+                index_error(a.err);
+              } else {
+                page = page_or_bad(a.s, a.c, b, pos, a.err);
+                off = pos - (int)fdiv((uint32_t)pos, a.c.fd_page) * a.c.page_size;
+              }
+            }
+            s_page[lane] = page;
+            s_off[lane] = off;
+          }
+        }
+        __syncthreads();
       }
-      const long long page = tok[u] >= 0 ? s_page[tok[u]] : -1;
-      if (page < 0) continue;
-      const int off = s_off[tok[u]];
-      const bool is_v = row[u] >= a.c.Hkv;
-      const int h = is_v ? row[u] - a.c.Hkv : row[u];
-      C* out = static_cast<C*>(is_v ? a.c.v : a.c.k) + (tid % G) * E +
-               (is_v ? page * a.c.vp + h * a.c.vh + off * a.c.vt : page * a.c.kp + h * a.c.kh + off * a.c.kt);
-      alignas(16) C y[E];
 #pragma unroll
-      for (int n = 0; n < E; ++n) y[n] = encode<T, C>(x[u][n], s);
-      if (a.vec) {
-        if constexpr (E * sizeof(C) == 16) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(y);
-        else if constexpr (E * sizeof(C) == 8) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
-        else *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<const uint32_t*>(y);
-      } else {
+      for (int u = 0; u < kAhead; ++u) {
+        float s = 1.f;
+        if (is_code<C>::value) {
+          float m = piece_amax(x[u], T());
 #pragma unroll
-        for (int n = 0; n < E; ++n) out[n] = y[n];
-      }
-      if (is_code<C>::value && tid % G == 0) {
-        if (is_v) a.c.vs[page * a.c.vsp + h * a.c.vsh + off * a.c.vst] = s;
-        else a.c.ks[page * a.c.ksp + h * a.c.ksh + off * a.c.kst] = s;
+          for (int o = 1; o < G; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          // fl(m / Q) the same way: neither Q's significand is all ones
+          constexpr float Q = code_max<C>();
+          s = m < 1e30f && m > 1e-20f ? quotient(m, Q, 1.f / Q) : __fdiv_rn(m, Q);
+          s = fmaxf(s, kScaleFloor);
+        }
+        const int t = base + u * a.side + tl;
+        if (!mine || t >= ntok) continue;
+        const long long page = s_page[t];
+        if (page < 0) continue;
+        const int off = s_off[t];
+        C* out = dst + page * dp + off * dt;
+        constexpr int W = E * sizeof(C) / 4;
+        uint32_t y[W];
+        encode_piece<T, C, E>(x[u], s, y);
+        if (a.vec) {
+          if constexpr (W == 4) *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2], y[3]);
+          else if constexpr (W == 2) *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[1]);
+          else *reinterpret_cast<uint32_t*>(out) = y[0];
+        } else {
+          alignas(16) C e[E];
+          memcpy(e, y, sizeof(e));
+#pragma unroll
+          for (int n = 0; n < E; ++n) out[n] = e[n];
+        }
+        if (is_code<C>::value && tid % G == 0) {
+          if (is_v) a.c.vs[page * a.c.vsp + h * a.c.vsh + off * a.c.vst] = s;
+          else a.c.ks[page * a.c.ksp + h * a.c.ksh + off * a.c.kst] = s;
+        }
       }
     }
   }
@@ -293,13 +352,16 @@ cudaError_t write_one(WriteArgs& a, cudaStream_t stream) {
   a.vec = mult(a.k, a.kt, a.kh, 0, sizeof(T), 16) && mult(a.v, a.vt, a.vh, 0, sizeof(T), 16) &&
           mult(a.c.k, a.c.kp, a.c.kh, a.c.kt, sizeof(C), nb) && mult(a.c.v, a.c.vp, a.c.vh, a.c.vt, sizeof(C), nb);
   a.ppt = 2 * a.c.Hkv * (D / E);
-  a.fd_ppt = make_fastdiv((uint32_t)a.ppt);
-  // a token per block while that does not fill the SMs, more tokens to share
-  // the lookups and deepen the loads beyond that
-  const int fill = 8 * num_sms();
-  a.tb = std::max(1, std::min(kMaxTok, a.s.total_q / fill));
+  const int rounds = (a.ppt + kThreads - 1) / kThreads;
+  a.per = rounds == 1 ? a.ppt : ((a.ppt + rounds - 1) / rounds + 31) / 32 * 32;
+  a.side = std::max(1, std::min(kMaxTok / kAhead, kThreads / a.per));
+  a.fd_per = make_fastdiv((uint32_t)a.per);
+  // a token per block while that does not fill the SMs, beyond that up to as
+  // many as the block's threads have pieces in flight for
+  a.tb = std::max(1, std::min(a.side * kAhead, a.s.total_q / (4 * num_sms())));
+  const int threads = (a.side * a.per + 31) / 32 * 32;
   return launch_serialized(cache_write_kernel<T, C, D>, dim3((unsigned)((a.s.total_q + a.tb - 1) / a.tb)),
-                           dim3(kThreads), 0, stream, a);
+                           dim3((unsigned)threads), 0, stream, a);
 }
 template <typename T, typename C>
 cudaError_t write_d(WriteArgs& a, cudaStream_t stream) {
