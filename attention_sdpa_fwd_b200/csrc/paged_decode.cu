@@ -12,21 +12,24 @@
 //    leaves unnormalised parts (O, max, sum) in the workspace, at most two per
 //    CTA, and merge_kernel, launched behind, adds them in a fixed order: no
 //    atomics, no state between calls.
-//  * Each warp runs on its own (two together where a unit has more than 16
-//    rows, a row tile each): it copies KS keys and values at a time with
+//  * Each warp runs on its own: it copies KS keys and values at a time with
 //    16-byte cp.async into its own ring of NST stages and never waits for
-//    other warps before the end of a unit.  Keys outside the visible range are
+//    another warp before the end of a unit.  Keys outside the visible range are
 //    filled with zeros without being read (their pages may be gone).
-//  * S = Q.K^T and O += P.V are mma.sync m16n8k16 tiles: at this arithmetic
-//    intensity the tensor pipe is far from its limit and register fragments
-//    save the trips through tensor memory.  The C fragment of S is the A
-//    fragment of P as it stands.
+//  * S^T = K.Q^T and O^T += V^T.P^T are mma.sync m16n8k16 tiles of 16 keys (16
+//    columns of V) by 8 rows: the few rows are the narrow side, K and V are
+//    converted once whatever the number of rows, and P^T becomes the second
+//    product's operand by a transpose of 8 x 8 blocks in registers.  (With the
+//    rows on the 16-wide side, as it was first, a unit of 4 rows took twice the
+//    products, exponentials and registers.)  At this arithmetic intensity the
+//    tensor pipe is far from its limit and register fragments save the trips
+//    through tensor memory.
 //
 // 8-bit codes go to f16 without rounding (every e4m3 and int8 value is one).
 // The order of d inside S's sum and of O's columns is free, so a lane takes the
 // codes of its fragments as 16-byte runs of a row: K[key][c D/4 ..] feeds all
-// k-steps of lane c of a quad, V[key][n D/8 ..] column n of every n8 tile, two
-// keys interleaved by byte permutes.  q is scaled by a power of two per row
+// k-steps of lane c of a quad, V[key][n D/8 ..] rows n and n + 8 of every V^T
+// tile, two keys interleaved by byte permutes.  q is scaled by a power of two per row
 // that puts its largest element in [2^14, 2^15), so f16 keeps it to 2^-39 of
 // that.  K's scale multiplies the score's column; V's goes into the exponent:
 //     t_j = x_j log2e + log2 vs_j,  p_j = 2^(t_j - m),  m = max t
@@ -64,39 +67,45 @@ struct DecodeArgs {
   PagedParams p;
   int limit;   // sequences of up to this many rows are this kernel's
   int whole;   // one CTA per unit, nothing split
+  // strides of a page (bytes; of the scales elements) and of a token, 32 bits each
+  uint32_t kp, vp, kt, vt, ksp, vsp, kst, vst;
+  int dense;   // a page's rows of a head follow each other
   float* ws_o;      // [2 * CTAs][rows][D]
   float2* ws_ml;    // [2 * CTAs][rows]
   int4* ws_unit;    // [units] CTAs that share a unit: first, last, slot of the first (0 or 1)
 };
 
-// MT: 16-row tiles of a unit.  MT warps share a stream of keys, a row tile each.
-template <int KV, int D, int MT>
+// NT: 8-row tiles of a unit.
+template <int KV, int D, int NT>
 struct Cfg {
   static constexpr bool kCodes = KV != KV_BF16;
   static constexpr int kElem = kCodes ? 1 : 2;
-  static constexpr int kStreams = kWarps / MT;
-  static constexpr int KS = !kCodes && D == 128 ? 16 : 32;       // keys of a stream's step
+  static constexpr int KS = !kCodes && D == 128 ? 16 : 32;       // keys of a warp's step
   static constexpr int kRow = D * kElem;
   static constexpr int kTile = KS * kRow;                        // K (or V) of a step
-  static constexpr int kScales = kCodes ? 4 * KS * 4 : 0;        // ks, vs, log2 vs, 1 / vs
+  static constexpr int kScales = kCodes ? 2 * KS * 4 : 0;        // ks, vs
   static constexpr int kStage = 2 * kTile + kScales;
-  static constexpr bool kQSmem = kCodes;                         // Q fragments in shared memory
-  static constexpr int kCtas = kCodes ? 3 : 2;                   // of an SM
-  static constexpr int NST = kCodes ? (D == 128 ? 1 + MT : 3) : 3 * MT;
-  static constexpr int kRows = 16 * MT;
+  static constexpr bool kQSmem = NT > 1;                         // Q fragments in shared memory
+  static constexpr int kCtas = kCodes && NT < 4 ? 3 : 2;         // of an SM
+  static constexpr int NST = kCodes ? (D == 128 ? (kCtas == 3 ? 2 : 3) : 3) : 3;
+  static constexpr int kRows = 8 * NT;
   static constexpr int kPitch = D + 4;
-  static constexpr int kRing = kStreams * NST * kStage;
-  static constexpr int kMergeBytes = kStreams * kRows * kPitch * 4;
-  static constexpr int kQ = kQSmem ? MT * (D / 16) * 32 * 16 : 0;
+  static constexpr int kRing = kWarps * NST * kStage;
+  static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
+  static constexpr int kQ = kQSmem ? NT * (D / 16) * 32 * 8 : 0;
   static constexpr int kBig = kRing > kMergeBytes ? kRing : kMergeBytes;
   static constexpr int oQ = kBig;
-  static constexpr int oML = oQ + kQ;                            // [kStreams][kRows] float2
-  static constexpr int kTotal = oML + kStreams * kRows * 8;
-  static constexpr int kKeys = kStreams * KS;                    // keys of a tile
+  static constexpr int oSk = oQ + kQ;                            // [kWarps][KS] float4: ks, log2 vs, 1 / vs of a step
+  static constexpr int oML = oSk + (kCodes ? kWarps * KS * 16 : 0);  // [kWarps][kRows] float2
+  static constexpr int kTotal = oML + kWarps * kRows * 8;
+  static constexpr int kKeys = kWarps * KS;                      // keys of a tile
   static_assert(kCtas * (kTotal + 1024) <= 233472, "shared memory of an SM");
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16_if(uint32_t dst, const void* src, bool live) {  // zeros where not live, nothing read
   const int n = live ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
@@ -126,6 +135,12 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   return r;
 }
 
+// An 8 x 8 matrix of 16-bit elements, a row's pair per lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (F16)
@@ -191,9 +206,9 @@ __device__ __forceinline__ long long div64(long long a, long long b) {
 // CTA that owns tile f of T split over G
 __device__ __forceinline__ int owner(long long f, long long T, int G) { return (int)div64((f + 1) * G - 1, T); }
 
-template <int KV, int D, int MT, bool MOD>
-__global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decode_kernel(const __grid_constant__ DecodeArgs a) {
-  using C = Cfg<KV, D, MT>;
+template <int KV, int D, int NT, bool MOD>
+__global__ void __launch_bounds__(kThreads, (Cfg<KV, D, NT>::kCtas)) paged_decode_kernel(const __grid_constant__ DecodeArgs a) {
+  using C = Cfg<KV, D, NT>;
   constexpr bool F16 = KV != KV_BF16;
   constexpr int KS = C::KS, NST = C::NST;
   constexpr float kShift = kOffset<F16>;
@@ -203,11 +218,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
   const PagedParams& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quad = lane >> 2, c = lane & 3;
-  const int stream = warp / MT, rt = warp % MT;  // stream of keys, row tile
-  auto stream_sync = [&] {
-    if constexpr (MT == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + stream), "n"(32 * MT) : "memory");
-  };
   grid_dep_wait();
   grid_dep_launch();  // the merge may start: it reads nothing of this call's inputs that still changes
 
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
   }
   const long long begin = cur;
 
-  const uint32_t ring = smem_u32(smem) + stream * (NST * C::kStage);
+  const uint32_t ring = smem_u32(smem) + warp * (NST * C::kStage);
   float* mrg = reinterpret_cast<float*>(smem);
   float2* s_ml = reinterpret_cast<float2*>(smem + C::oML);
 
@@ -275,24 +285,21 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
     const int hk = (int)div64(cur - F, u.nt);
     const int tile0 = (int)((cur - F) - (long long)hk * u.nt);
     const int ntile = (int)min((long long)(u.nt - tile0), end - cur);
-    const int base = u.lo16 + tile0 * C::kKeys + stream * KS;  // this stream's first key
+    const int base = u.lo16 + tile0 * C::kKeys + warp * KS;  // this warp's first key
     const int khi = u.hi, klo = u.lo;
 
-    // ---- the ring: one step is KS keys and values of this stream, each of its warps copies a share of the rows
-    const uint8_t* kp = static_cast<const uint8_t*>(p.c.k) + (long long)hk * p.c.kh * C::kElem;
-    const uint8_t* vp = static_cast<const uint8_t*>(p.c.v) + (long long)hk * p.c.vh * C::kElem;
+    // ---- the ring: one step is KS keys and values of this warp
     constexpr int kPieces = C::kRow / 16;  // of a row
-    constexpr int kPass = MT * 32 / kPieces;  // rows the stream's warps copy at once
-    const int piece = lane % kPieces, r0 = rt * (32 / kPieces) + lane / kPieces;
-    const long long kstep = p.c.kt * (kPass * C::kElem), vstep = p.c.vt * (kPass * C::kElem);
-    kp += (long long)r0 * p.c.kt * C::kElem + piece * 16;
-    vp += (long long)r0 * p.c.vt * C::kElem + piece * 16;
-    // the next step's pages: where this lane's first row of each 16 tokens is
-    const uint8_t *kq[KS / 16], *vq[KS / 16];
-    const float *ksq, *vsq;
-    // Page numbers are fetched 32 sixteen-token groups at a time, a lane per
-    // group, one such span ahead of its use.
-    constexpr int kGroups = KS / 16, kSpan = 32 / kGroups;
+    constexpr int kPass = 32 / kPieces;    // rows the warp copies at once
+    constexpr int kGroups = KS / 16;       // runs of 16 tokens, each inside a page
+    const int piece = lane % kPieces, r0 = lane / kPieces;
+    const uint8_t* kp = static_cast<const uint8_t*>(p.c.k) + (long long)hk * p.c.kh * C::kElem + r0 * a.kt + piece * 16;
+    const uint8_t* vp = static_cast<const uint8_t*>(p.c.v) + (long long)hk * p.c.vh * C::kElem + r0 * a.vt + piece * 16;
+    const float* ksp = F16 ? p.c.ks + (long long)hk * p.c.ksh : nullptr;
+    const float* vsp = F16 ? p.c.vs + (long long)hk * p.c.vsh : nullptr;
+    // Page numbers are fetched 32 runs at a time, a lane per run, one such span
+    // ahead of its use.
+    constexpr int kSpan = 32 / kGroups;
     auto fetch = [&](int span) {
       const int step = span * kSpan + lane / kGroups;
       const int t = base + step * C::kKeys + 16 * (lane % kGroups);
@@ -300,45 +307,63 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
     };
     int pages = fetch(0), pages_next = fetch(1);
     pages = max(0, good_page(p.c, pages, p.err));
-    // where this lane's first row of each 16 tokens of a step is
+    // The next step: where this lane's first row of each run is, and its key's
+    // scales.  Inside a page 32 bits do (the host checks that).
+    const uint8_t *kq[kGroups], *vq[kGroups];
+    const float *ksq, *vsq;
     auto lookup = [&](int step) {
       if (step > 0 && step % kSpan == 0) {
         pages = max(0, good_page(p.c, pages_next, p.err));
         pages_next = fetch(step / kSpan + 1);
       }
       const int t0 = base + step * C::kKeys;
+      uint32_t off = t0 - fdiv((uint32_t)t0, p.c.fd_page) * p.c.page_size;
+      if constexpr (F16) {
+        const uint32_t pg = __shfl_sync(0xffffffffu, pages, (step % kSpan) * kGroups + lane / 16);
+        uint32_t o = off + lane;
+        if (o >= (uint32_t)p.c.page_size) o -= p.c.page_size;  // the second run's page (a page has 16 tokens or more)
+        ksq = ksp + (uint64_t)pg * a.ksp + o * a.kst;
+        vsq = vsp + (uint64_t)pg * a.vsp + o * a.vst;
+      }
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const int t = t0 + 16 * g;
-        const long long pg = __shfl_sync(0xffffffffu, pages, (step % kSpan) * kGroups + g);
-        const int off = t - (int)fdiv((uint32_t)t, p.c.fd_page) * p.c.page_size;
-        kq[g] = kp + (pg * p.c.kp + off * p.c.kt) * C::kElem;
-        vq[g] = vp + (pg * p.c.vp + off * p.c.vt) * C::kElem;
-        if (F16 && lane / 16 == g) {
-          ksq = p.c.ks + pg * p.c.ksp + hk * p.c.ksh + (off + lane % 16) * p.c.kst;
-          vsq = p.c.vs + pg * p.c.vsp + hk * p.c.vsh + (off + lane % 16) * p.c.vst;
-        }
+        const uint32_t pg = __shfl_sync(0xffffffffu, pages, (step % kSpan) * kGroups + g);
+        kq[g] = kp + (uint64_t)pg * a.kp + off * a.kt;
+        vq[g] = vp + (uint64_t)pg * a.vp + off * a.vt;
+        off += 16;
+        if (off >= (uint32_t)p.c.page_size) off -= p.c.page_size;
       }
     };
     auto issue = [&](int step) {
       if (step < ntile) {
         const uint32_t st = ring + (step % NST) * C::kStage;
         const int t0 = base + step * C::kKeys;
-        const bool all = t0 >= klo && t0 + KS <= khi;
+        if (a.dense && t0 >= klo && t0 + KS <= khi) {
+          // rows of a page that follow each other, all of them seen: constant offsets
 #pragma unroll
-        for (int i = 0; i < KS / kPass; ++i) {
-          const int r = i * kPass + r0, g = (i * kPass) / 16;
-          const bool live = all || (t0 + r >= klo && t0 + r < khi);
-          cp16(st + k_off<KV, D>(r, piece), kq[g], live);
-          cp16(st + C::kTile + v_off<KV, D>(r, piece), vq[g], live);
-          kq[g] += kstep;
-          vq[g] += vstep;
-        }
-        if (F16 && rt == 0) {  // KS == 32: a lane per key
-          const bool live = all || (t0 + lane >= klo && t0 + lane < khi);
-          const uint32_t sc = st + 2 * C::kTile + lane * 4;
-          cp4(sc, ksq, live);
-          cp4(sc + KS * 4, vsq, live);
+          for (int i = 0; i < KS / kPass; ++i) {
+            const int r = i * kPass, g = r / 16;
+            cp16(st + k_off<KV, D>(r + r0, piece), kq[g] + (r % 16) * C::kRow);
+            cp16(st + C::kTile + v_off<KV, D>(r + r0, piece), vq[g] + (r % 16) * C::kRow);
+          }
+          if constexpr (F16) {  // KS == 32: a lane per key
+            cp4(st + 2 * C::kTile + lane * 4, ksq, true);
+            cp4(st + 2 * C::kTile + (KS + lane) * 4, vsq, true);
+          }
+        } else {
+#pragma unroll 4
+          for (int i = 0; i < KS / kPass; ++i) {
+            const int r = i * kPass, g = r / 16;
+            const bool live = t0 + r + r0 >= klo && t0 + r + r0 < khi;
+            const uint8_t *kr = g == 0 ? kq[0] : kq[kGroups - 1], *vr = g == 0 ? vq[0] : vq[kGroups - 1];
+            cp16_if(st + k_off<KV, D>(r + r0, piece), kr + (r % 16) * a.kt, live);
+            cp16_if(st + C::kTile + v_off<KV, D>(r + r0, piece), vr + (r % 16) * a.vt, live);
+          }
+          if constexpr (F16) {
+            const bool live = t0 + lane >= klo && t0 + lane < khi;
+            cp4(st + 2 * C::kTile + lane * 4, ksq, live);
+            cp4(st + 2 * C::kTile + (KS + lane) * 4, vsq, live);
+          }
         }
       }
       cp_commit();
@@ -350,23 +375,17 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
     }
     lookup(NST - 1);
 
-    // ---- Q as A fragments: row r of the unit is token r / group, head r % group
-    uint32_t qf[C::kQSmem ? 1 : D / 16][4];
-    float xscale[2];  // what turns the accumulator of a row into its score
-    int pos[2];
-    float slope[2];
-    const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(p.q);
-    uint32_t* s_q = reinterpret_cast<uint32_t*>(smem + C::oQ) + rt * (D / 16) * 128;
+    // ---- Q^T as B fragments: row r of the unit is token r / group, head r % group
+    uint32_t qf[C::kQSmem ? 1 : D / 16][2];
+    uint32_t* s_q = reinterpret_cast<uint32_t*>(smem + C::oQ);
+    float* s_x = reinterpret_cast<float*>(s_ml);  // a row's power of two, until the parts need the place
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = rt * 16 + e * 8 + quad;
+    for (int t = 0; t < NT; ++t) {
+      const int r = t * 8 + quad;
       const int i = r / p.group, g = r - i * p.group;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (long long)(u.s.q0 + i) * p.qt +
+                                 (long long)(hk * p.group + g) * p.qh;
       const bool live = r < u.rows;
-      const int h = hk * p.group + g;
-      const __nv_bfloat16* src = qb + (long long)(u.s.q0 + i) * p.qt + (long long)h * p.qh;
-      pos[e] = u.s.L - u.s.n + i;
-      slope[e] = MOD && p.slopes && live ? __ldg(p.slopes + h) : 0.f;
-      xscale[e] = p.scale;
       uint32_t w[D / 8];  // this lane's D / 4 elements, in pairs
       if constexpr (F16) {
 #pragma unroll
@@ -384,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
         // 2^k with top 2^k in [2^14, 2^15), k within what a float holds
         const int ex = top > 0.f && top < INFINITY ? min(126, max(-126, 141 - (int)(__float_as_uint(top) >> 23))) : 0;
         const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
-        xscale[e] *= __uint_as_float((uint32_t)(127 - ex) << 23);
+        if (c == 0) s_x[warp * C::kRows + r] = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
           const __half2 hh = __floats2half2_rn(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
@@ -395,177 +414,205 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
         for (int k = 0; k < D / 8; ++k)
           w[k] = live ? __ldg(reinterpret_cast<const unsigned int*>(src + 16 * (k >> 1) + 8 * (k & 1) + 2 * c)) : 0u;
       }
-      // pair 2s is a0 / a1 of k-step s, pair 2s + 1 is a2 / a3
+      // pairs 2s and 2s + 1 are b0 and b1 of k-step s
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
         if constexpr (!C::kQSmem) {
-          qf[s][e] = w[2 * s];
-          qf[s][2 + e] = w[2 * s + 1];
-        } else if (s % C::kStreams == stream) {  // the streams' warps of a row tile have the same: each writes a share
-          s_q[(s * 32 + lane) * 4 + e] = w[2 * s];
-          s_q[(s * 32 + lane) * 4 + 2 + e] = w[2 * s + 1];
+          qf[s][0] = w[2 * s];
+          qf[s][1] = w[2 * s + 1];
+        } else if (s % kWarps == warp) {  // every warp has the same: each writes a share
+          *reinterpret_cast<uint2*>(s_q + ((t * (D / 16) + s) * 32 + lane) * 2) = make_uint2(w[2 * s], w[2 * s + 1]);
         }
       }
     }
     if constexpr (C::kQSmem) __syncthreads();
+    else __syncwarp();
+    // this lane's columns of S^T: rows t * 8 + 2 c + e
+    float xscale[NT][2];  // what turns an accumulator into its score
+    float slope[MOD ? NT : 1][2];
+    int pos[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = t * 8 + 2 * c + e;
+        const int i = r / p.group, g = r - i * p.group;
+        pos[t][e] = u.s.L - u.s.n + i;
+        if constexpr (MOD) slope[t][e] = p.slopes && r < u.rows ? __ldg(p.slopes + hk * p.group + g) : 0.f;
+        xscale[t][e] = p.scale * (F16 ? s_x[warp * C::kRows + r] : 1.f);
+        if constexpr (!MOD) xscale[t][e] *= kLog2e;
+      }
 
-    float o[D / 8][4];
-    float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[NT][D / 16][4];
+    float mx[NT][2], l[NT][2];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int t = 0; t < NT; ++t) {
+      mx[t][0] = mx[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
+    }
     const int pos_first = u.s.L - u.s.n, pos_last = u.s.L - 1;
     const float icap2 = MOD && p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
 
     for (int step = 0; step < ntile; ++step) {
       cp_wait<NST - 2>();
-      stream_sync();
+      __syncwarp();
       const uint32_t st = ring + (step % NST) * C::kStage;
       const int t0 = base + step * C::kKeys;
       float* sc = reinterpret_cast<float*>(smem + (st - smem_u32(smem)) + 2 * C::kTile);
+      float4* sk = reinterpret_cast<float4*>(smem + C::oSk) + warp * KS;
       if constexpr (F16) {
-        // log2 vs and 1 / vs of this lane's key (every warp of the stream
-        // writes the same); a key not read counts as scale 1
+        // what this lane's key needs: ks, log2 vs, 1 / vs; a key not read counts as scale 1
         const int t = t0 + lane;
         const float vs = t >= klo && t < khi ? sc[KS + lane] : 1.f;
         float lg;
         asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(vs));
-        sc[2 * KS + lane] = lg;
-        sc[3 * KS + lane] = rcp_approx(vs);
+        sk[lane] = make_float4(sc[lane], lg, rcp_approx(vs), 0.f);
       }
       issue(step + NST - 1);
       lookup(step + NST);
       if (t0 >= khi || t0 + KS <= klo) continue;  // nothing of it is seen
       if constexpr (F16) __syncwarp();
       const bool edge = t0 + KS - 1 > pos_first || t0 < klo || (p.window > 0 && t0 <= pos_last - p.window);
-      // ---- S = Q.K^T
-      float s[KS / 8][4];
+      // 16 keys at a time, a rolled loop: unrolled it costs 40 registers and an
+      // occupancy step
+#pragma unroll 1
+      for (int k0 = 0; k0 < KS; k0 += 16) {
+        // ---- S^T = K.Q^T, 16 keys by 8 rows
+        float s[NT][4];
 #pragma unroll
-      for (int n = 0; n < KS / 8; ++n)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
-      if constexpr (F16) {
-        uint32_t w[KS / 8][D / 16];
-#pragma unroll
-        for (int n = 0; n < KS / 8; ++n)
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
-            const uint4 x = lds16(st + k_off<KV, D>(n * 8 + quad, c * (D / 64) + i));
-            w[n][4 * i] = x.x; w[n][4 * i + 1] = x.y; w[n][4 * i + 2] = x.z; w[n][4 * i + 3] = x.w;
-          }
-#pragma unroll
-        for (int ss = 0; ss < D / 16; ++ss) {
-          const uint4 x = lds16(smem_u32(s_q) + (ss * 32 + lane) * 16);
-          const uint32_t q4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int n = 0; n < KS / 8; ++n) {
-            uint32_t b0, b1;
-            codes4<KV>(w[n][ss], b0, b1);
-            mma<F16>(s[n], q4, b0, b1);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int sp = 0; sp < D / 32; ++sp)
-#pragma unroll
-          for (int n = 0; n < KS / 8; ++n) {
-            uint32_t r[4];
-            ldsm4(st + k_off<KV, D>(n * 8 + (lane & 7), 4 * sp + (lane >> 3)), r);
-            mma<F16>(s[n], qf[2 * sp], r[0], r[1]);
-            mma<F16>(s[n], qf[2 * sp + 1], r[2], r[3]);
-          }
-      }
-      // ---- scores in log2 units, running max, P
-      uint32_t pf[KS / 16][4];
-      float iv[F16 ? KS / 8 : 1][2];
-      float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int n = 0; n < KS / 8; ++n) {
-        const int kk = n * 8 + 2 * c;
-        float ks2[2] = {1.f, 1.f}, lv2[2] = {0.f, 0.f};
+          for (int k = 0; k < 4; ++k) s[t][k] = 0.f;
+        auto q_frag = [&](int t, int ss) {
+          if constexpr (C::kQSmem) return lds8(smem_u32(s_q) + ((t * (D / 16) + ss) * 32 + lane) * 8);
+          else return make_uint2(qf[ss][0], qf[ss][1]);
+        };
         if constexpr (F16) {
-          const float2 x = *reinterpret_cast<const float2*>(sc + kk);
-          const float2 y = *reinterpret_cast<const float2*>(sc + 2 * KS + kk);
-          const float2 z = *reinterpret_cast<const float2*>(sc + 3 * KS + kk);
-          ks2[0] = x.x; ks2[1] = x.y; lv2[0] = y.x; lv2[1] = y.y;
-          iv[n][0] = z.x; iv[n][1] = z.y;
-        }
+          uint32_t w[2][D / 16];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int e = k >> 1, j = t0 + kk + (k & 1);
-          if constexpr (MOD) {
-            float y = s[n][k] * xscale[e] * ks2[k & 1];
-            if (p.softcap > 0.f)  // c tanh(y / c) = c - 2 c / (1 + e^(2 y / c))
-              y = fmaf(-2.f * p.softcap, rcp_approx(1.f + ex2_approx(y * icap2)), p.softcap);
-            y = fmaf(slope[e], (float)(j - pos[e]), y);
-            s[n][k] = fmaf(y, kLog2e, lv2[k & 1]);
-          } else if constexpr (F16) {
-            s[n][k] = fmaf(s[n][k] * ks2[k & 1], xscale[e] * kLog2e, lv2[k & 1]);
-          } else {
-            s[n][k] *= xscale[e] * kLog2e;
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+              const uint4 x = lds16(st + k_off<KV, D>(k0 + y * 8 + quad, c * (D / 64) + i));
+              w[y][4 * i] = x.x; w[y][4 * i + 1] = x.y; w[y][4 * i + 2] = x.z; w[y][4 * i + 3] = x.w;
+            }
+#pragma unroll
+          for (int ss = 0; ss < D / 16; ++ss) {
+            uint32_t a4[4];
+            codes4<KV>(w[0][ss], a4[0], a4[2]);
+            codes4<KV>(w[1][ss], a4[1], a4[3]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const uint2 q = q_frag(t, ss);
+              mma<F16>(s[t], a4, q.x, q.y);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int ss = 0; ss < D / 16; ++ss) {
+            uint32_t a4[4];
+            ldsm4(st + k_off<KV, D>(k0 + (lane & 15), 2 * ss + (lane >> 4)), a4);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const uint2 q = q_frag(t, ss);
+              mma<F16>(s[t], a4, q.x, q.y);
+            }
           }
         }
-      }
-      if (edge) {
+        // ---- scores in log2 units; this lane's keys are k0 + quad and + 8
+        float iv[2] = {1.f, 1.f}, ks2[2] = {1.f, 1.f}, lv2[2] = {0.f, 0.f};
+        if constexpr (F16) {
 #pragma unroll
-        for (int n = 0; n < KS / 8; ++n)
+          for (int y = 0; y < 2; ++y) {
+            const float4 x = sk[k0 + y * 8 + quad];
+            ks2[y] = x.x;
+            lv2[y] = x.y;
+            iv[y] = x.z;
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int j = t0 + n * 8 + 2 * c + (k & 1);
-            if (j > pos[k >> 1] || (p.window > 0 && j <= pos[k >> 1] - p.window)) s[n][k] = -INFINITY;
+            const int e = k & 1, y2 = k >> 1;
+            if constexpr (MOD) {
+              float y = s[t][k] * xscale[t][e] * ks2[y2];
+              if (p.softcap > 0.f)  // c tanh(y / c) = c - 2 c / (1 + e^(2 y / c))
+                y = fmaf(-2.f * p.softcap, rcp_approx(1.f + ex2_approx(y * icap2)), p.softcap);
+              y = fmaf(slope[t][e], (float)(t0 + k0 + y2 * 8 + quad - pos[t][e]), y);
+              s[t][k] = fmaf(y, kLog2e, lv2[y2]);
+            } else if constexpr (F16) {
+              s[t][k] = fmaf(s[t][k] * ks2[y2], xscale[t][e], lv2[y2]);
+            } else {
+              s[t][k] *= xscale[t][e];
+            }
           }
-      }
+        if (edge) {
 #pragma unroll
-      for (int n = 0; n < KS / 8; ++n)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) top[k >> 1] = fmaxf(top[k >> 1], s[n][k]);
-      bool grow = false;
-      float al[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-        al[e] = 1.f;
-        if (top[e] > mx[e] + kLag<F16>) {  // from -inf too; false while both are
-          al[e] = ex2_approx(mx[e] - top[e]);
-          mx[e] = top[e];
-          grow = true;
+            for (int k = 0; k < 4; ++k) {
+              const int j = t0 + k0 + (k >> 1) * 8 + quad;
+              if (j > pos[t][k & 1] || (p.window > 0 && j <= pos[t][k & 1] - p.window)) s[t][k] = -INFINITY;
+            }
         }
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-        l[0] *= al[0];
-        l[1] *= al[1];
+        // ---- the running max: only when a score passes it by the lag are the lanes compared
+        bool grow = false;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= al[0]; o[i][1] *= al[0];
-          o[i][2] *= al[1]; o[i][3] *= al[1];
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) grow |= fmaxf(s[t][e], s[t][2 + e]) > mx[t][e] + kLag<F16>;  // from -inf too
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(s[t][e], s[t][2 + e]);
+#pragma unroll
+              for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+              if (top > mx[t][e] + kLag<F16>) {
+                const float al = ex2_approx(mx[t][e] - top);
+                mx[t][e] = top;
+                l[t][e] *= al;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  o[t][i][e] *= al;
+                  o[t][i][2 + e] *= al;
+                }
+              }
+            }
         }
-      }
-      const float ms[2] = {mx[0] == -INFINITY ? 0.f : mx[0] - kShift, mx[1] == -INFINITY ? 0.f : mx[1] - kShift};
+        // ---- P^T as B fragments: a row's two keys in one register by a transpose
+        uint32_t pf[NT][2];
 #pragma unroll
-      for (int n = 0; n < KS / 8; ++n) {
-        float w[4];
+        for (int t = 0; t < NT; ++t) {
+          const float ms[2] = {mx[t][0] == -INFINITY ? 0.f : mx[t][0] - kShift,
+                               mx[t][1] == -INFINITY ? 0.f : mx[t][1] - kShift};
+          float w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          w[k] = ex2_approx(s[n][k] - ms[k >> 1]);
-          if constexpr (F16) l[k >> 1] = fmaf(w[k], iv[n][k & 1], l[k >> 1]);
-          else l[k >> 1] += w[k];
+          for (int k = 0; k < 4; ++k) {
+            w[k] = ex2_approx(s[t][k] - ms[k & 1]);
+            if constexpr (F16) l[t][k & 1] = fmaf(w[k], iv[k >> 1], l[t][k & 1]);
+            else l[t][k & 1] += w[k];
+          }
+          uint32_t lo, hi;
+          if constexpr (F16) {
+            const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
+            memcpy(&lo, &h0, 4);
+            memcpy(&hi, &h1, 4);
+          } else {
+            lo = pack_bf16x2(w[0], w[1]);
+            hi = pack_bf16x2(w[2], w[3]);
+          }
+          pf[t][0] = transpose8(lo);
+          pf[t][1] = transpose8(hi);
         }
-        if constexpr (F16) {
-          const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
-          memcpy(&pf[n >> 1][(n & 1) * 2], &h0, 4);
-          memcpy(&pf[n >> 1][(n & 1) * 2 + 1], &h1, 4);
-        } else {
-          pf[n >> 1][(n & 1) * 2] = pack_bf16x2(w[0], w[1]);
-          pf[n >> 1][(n & 1) * 2 + 1] = pack_bf16x2(w[2], w[3]);
-        }
-      }
-      // ---- O += P.V
-      const uint32_t vt = st + C::kTile;
-#pragma unroll
-      for (int kg = 0; kg < KS / 16; ++kg) {
-        const int k0 = kg * 16;
+        // ---- O^T += V^T.P^T
+        const uint32_t vt = st + C::kTile;
         if constexpr (F16) {
           constexpr int W = D / 32;  // words of a lane's run of a row
           uint32_t w[4][W];
@@ -582,54 +629,62 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
           }
 #pragma unroll
           for (int i = 0; i < W; ++i) {
-            uint32_t b0[4], b1[4];
-            codes4<KV>(__byte_perm(w[0][i], w[1][i], 0x5140), b0[0], b0[1]);
-            codes4<KV>(__byte_perm(w[0][i], w[1][i], 0x7362), b0[2], b0[3]);
-            codes4<KV>(__byte_perm(w[2][i], w[3][i], 0x5140), b1[0], b1[1]);
-            codes4<KV>(__byte_perm(w[2][i], w[3][i], 0x7362), b1[2], b1[3]);
+            // columns 4 i .. 4 i + 3 of the run: two tiles, column 2 j in rows 0-7, 2 j + 1 in rows 8-15
+            uint32_t a4[2][4];
+            codes4<KV>(__byte_perm(w[0][i], w[1][i], 0x5140), a4[0][0], a4[0][1]);
+            codes4<KV>(__byte_perm(w[0][i], w[1][i], 0x7362), a4[1][0], a4[1][1]);
+            codes4<KV>(__byte_perm(w[2][i], w[3][i], 0x5140), a4[0][2], a4[0][3]);
+            codes4<KV>(__byte_perm(w[2][i], w[3][i], 0x7362), a4[1][2], a4[1][3]);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) mma<F16>(o[4 * i + y], pf[kg], b0[y], b1[y]);
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) mma<F16>(o[t][2 * i + y], a4[y], pf[t][0], pf[t][1]);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            uint32_t r[4];
-            ldsm4t(vt + v_off<KV, D>(k0 + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * i + (lane >> 4)), r);
-            mma<F16>(o[2 * i], pf[kg], r[0], r[1]);
-            mma<F16>(o[2 * i + 1], pf[kg], r[2], r[3]);
+            uint32_t a4[4];
+            ldsm4t(vt + v_off<KV, D>(k0 + (lane & 7) + (lane >> 4) * 8, 2 * i + ((lane >> 3) & 1)), a4);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma<F16>(o[t][i], a4, pf[t][0], pf[t][1]);
           }
         }
       }
     }
     cp_wait<0>();
 
-    // ---- the streams' parts into one
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-      if (c == 0) s_ml[stream * C::kRows + rt * 16 + e * 8 + quad] = make_float2(mx[e], l[e]);
-    }
+    // ---- the warps' parts into one
     __syncthreads();  // every ring is drained: its space holds the parts now
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = rt * 16 + e * 8 + quad;
-      float top = -INFINITY;
-      for (int w = 0; w < C::kStreams; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
-      const float f = mx[e] == -INFINITY ? 0.f : ex2_approx(mx[e] - top);
-      float* dst = mrg + (stream * C::kRows + r) * C::kPitch;
-      if (r < u.rows) {
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          if constexpr (F16) {
-            dst[(D / 8) * (2 * c) + i] = o[i][2 * e] * f;
-            dst[(D / 8) * (2 * c + 1) + i] = o[i][2 * e + 1] * f;
-          } else {
-            *reinterpret_cast<float2*>(dst + 8 * i + 2 * c) = make_float2(o[i][2 * e] * f, o[i][2 * e + 1] * f);
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], x);
+        if (quad == 0) s_ml[warp * C::kRows + t * 8 + 2 * c + e] = make_float2(mx[t][e], l[t][e]);
+      }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = t * 8 + 2 * c + e;
+        float top = -INFINITY;
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
+        const float f = mx[t][e] == -INFINITY ? 0.f : ex2_approx(mx[t][e] - top);
+        float* dst = mrg + (warp * C::kRows + r) * C::kPitch;
+        if (r < u.rows) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            if constexpr (F16) {
+              *reinterpret_cast<float2*>(dst + (D / 8) * quad + 2 * i) = make_float2(o[t][i][e] * f, o[t][i][2 + e] * f);
+            } else {
+              dst[16 * i + quad] = o[t][i][e] * f;
+              dst[16 * i + 8 + quad] = o[t][i][2 + e] * f;
+            }
           }
         }
       }
-    }
     __syncthreads();
     const bool complete = ntile == u.nt;
     const long long slot = 2LL * blockIdx.x + (cur == begin ? 0 : 1);
@@ -639,9 +694,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, MT>::kCtas)) paged_decod
     for (int i = tid; i < u.rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
       float top = -INFINITY, den = 0.f;
-      for (int w = 0; w < C::kStreams; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < C::kStreams; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float2 ml = s_ml[w * C::kRows + r];
         if (ml.x != -INFINITY) den = fmaf(ex2_approx(ml.x - top), ml.y, den);
         const float4 y = *reinterpret_cast<const float4*>(mrg + (w * C::kRows + r) * C::kPitch + x);
@@ -753,26 +808,33 @@ cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
   return e;
 }
 
-template <int KV, int D, int MT>
+template <int KV, int D, int NT>
 cudaError_t decode_one(DecodeArgs& a, bool mod, int ctas, cudaStream_t stream) {
-  using C = Cfg<KV, D, MT>;
-  auto kern = mod ? paged_decode_kernel<KV, D, MT, true> : paged_decode_kernel<KV, D, MT, false>;
+  using C = Cfg<KV, D, NT>;
+  auto kern = mod ? paged_decode_kernel<KV, D, NT, true> : paged_decode_kernel<KV, D, NT, false>;
   static std::atomic<uint64_t> done[2];
   cudaError_t e = allow_smem(kern, C::kTotal, done[mod]);
   if (e != cudaSuccess) return e;
   e = launch_serialized(kern, dim3((unsigned)ctas), dim3(kThreads), (size_t)C::kTotal, stream, a);
   if (e != cudaSuccess || a.whole) return e;
-  return launch_serialized(paged_merge_kernel<D, C::kRows>, dim3((unsigned)(a.p.s.B * a.p.c.Hkv)),
-                           dim3(kThreads), 0, stream, a, kOffset<KV != KV_BF16>);
+  return launch_serialized(paged_merge_kernel<D, C::kRows>, dim3((unsigned)(a.p.s.B * a.p.c.Hkv)), dim3(kThreads), 0,
+                           stream, a, kOffset<KV != KV_BF16>);
 }
 template <int KV, int D>
 cudaError_t decode_rows(DecodeArgs& a, bool mod, int ctas, cudaStream_t stream) {
-  return a.limit <= 16 ? decode_one<KV, D, 1>(a, mod, ctas, stream) : decode_one<KV, D, 2>(a, mod, ctas, stream);
+  switch (a.limit) {
+    case 8: return decode_one<KV, D, 1>(a, mod, ctas, stream);
+    case 16: return decode_one<KV, D, 2>(a, mod, ctas, stream);
+    default: return decode_one<KV, D, 4>(a, mod, ctas, stream);
+  }
 }
 
-// Rows a call's sequences may have here: 16 (one row tile) when no sequence
-// can have more, else 32.
-int row_limit(const PagedParams& p) { return (long long)p.s.max_q * p.group <= 16 ? 16 : kDecodeRows; }
+// Rows a call's sequences may have here: the fewest row tiles that hold the
+// bound max_q gives, at most 32 rows.
+int row_limit(const PagedParams& p) {
+  const long long rows = (long long)p.s.max_q * p.group;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : kDecodeRows;
+}
 
 // One CTA per unit and no merge launch where the caches are so short that
 // splitting them would cost more than it gives.  TODO-FIGURES
@@ -780,7 +842,7 @@ bool whole_units(const PagedParams& p) { return (long long)p.s.max_pages * p.c.p
 
 // One resident wave.
 int decode_ctas(const PagedParams& p) {
-  return num_sms() * (p.c.dtype != SDPA_CACHE_BF16 ? 3 : 2);
+  return num_sms() * (p.c.dtype != SDPA_CACHE_BF16 && row_limit(p) < 32 ? 3 : 2);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -796,6 +858,11 @@ int paged_decode_check(const PagedParams& p, sdpa_dtype_t dtype) {
   const long long bytes[] = {c.kp * es, c.kh * es, c.kt * es, c.vp * es, c.vh * es, c.vt * es, p.qt * 2, p.qh * 2};
   for (long long x : bytes)
     if (x % 16 != 0) return SDPA_ERR_MISALIGNED;
+  // strides of a page, and offsets inside one, in 32 bits
+  const long long wide[] = {c.kp * es, c.vp * es, c.kt * es * c.page_size, c.vt * es * c.page_size, c.ksp, c.vsp,
+                            c.kst * c.page_size, c.vst * c.page_size};
+  for (long long x : wide)
+    if (x > 0x7fffffffLL) return SDPA_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) | reinterpret_cast<uintptr_t>(p.q)) % 16 != 0 ||
       reinterpret_cast<uintptr_t>(p.out) % 8 != 0 || p.ot % 4 != 0 || p.oh % 4 != 0)
     return SDPA_ERR_MISALIGNED;
@@ -824,6 +891,11 @@ cudaError_t launch_paged_decode(const PagedParams& p, void* ws, cudaStream_t str
     w += up256(slots * rows * 8);
     a.ws_unit = reinterpret_cast<int4*>(w);
   }
+  const CacheView& c = p.c;
+  const uint32_t es = c.dtype == SDPA_CACHE_BF16 ? 2 : 1;
+  a.kp = (uint32_t)(c.kp * es); a.vp = (uint32_t)(c.vp * es); a.kt = (uint32_t)(c.kt * es); a.vt = (uint32_t)(c.vt * es);
+  a.ksp = (uint32_t)c.ksp; a.vsp = (uint32_t)c.vsp; a.kst = (uint32_t)c.kst; a.vst = (uint32_t)c.vst;
+  a.dense = c.kt == c.d && c.vt == c.d;
   const bool mod = p.softcap > 0.f || p.slopes != nullptr;
   const bool wide = p.c.d == 128;
   switch (p.c.dtype) {
