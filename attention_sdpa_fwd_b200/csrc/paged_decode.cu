@@ -86,7 +86,7 @@ struct Cfg {
   static constexpr int kScales = kCodes ? 2 * KS * 4 : 0;        // ks, vs
   static constexpr int kStage = 2 * kTile + kScales;
   static constexpr bool kQSmem = NT > 1;                         // Q fragments in shared memory
-  static constexpr int kCtas = kCodes && NT < 4 ? 3 : 2;         // of an SM
+  static constexpr int kCtas = kCodes && NT < 3 ? 3 : 2;         // of an SM
   static constexpr int NST = kCodes ? (D == 128 ? (kCtas == 3 ? 2 : 3) : 3) : 3;
   static constexpr int kRows = 8 * NT;
   static constexpr int kPitch = D + 4;
@@ -306,6 +306,28 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, NT>::kCtas)) paged_decod
       return step < ntile && t < khi && t + 16 > klo ? page_entry(p.s, p.c, b, t) : 0;
     };
     int pages = fetch(0), pages_next = fetch(1);
+    // Q's rows are on their way before the pages are waited for: row r of the
+    // unit is token r / group, head r % group
+    uint32_t qw[NT][D / 8];  // of row t * 8 + quad: this lane's D / 4 elements, in pairs
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = t * 8 + quad;
+      const int i = r / p.group, g = r - i * p.group;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (long long)(u.s.q0 + i) * p.qt +
+                                 (long long)(hk * p.group + g) * p.qh;
+      if constexpr (F16) {
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (r < u.rows) x = __ldg(reinterpret_cast<const uint4*>(src + c * (D / 4) + k * 8));
+          qw[t][4 * k] = x.x; qw[t][4 * k + 1] = x.y; qw[t][4 * k + 2] = x.z; qw[t][4 * k + 3] = x.w;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k)
+          qw[t][k] = r < u.rows ? __ldg(reinterpret_cast<const unsigned int*>(src + 16 * (k >> 1) + 8 * (k & 1) + 2 * c)) : 0u;
+      }
+    }
     pages = max(0, good_page(p.c, pages, p.err));
     // The next step: where this lane's first row of each run is, and its key's
     // scales.  Inside a page 32 bits do (the host checks that).
@@ -375,25 +397,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, NT>::kCtas)) paged_decod
     }
     lookup(NST - 1);
 
-    // ---- Q^T as B fragments: row r of the unit is token r / group, head r % group
+    // ---- Q^T as B fragments
     uint32_t qf[C::kQSmem ? 1 : D / 16][2];
     uint32_t* s_q = reinterpret_cast<uint32_t*>(smem + C::oQ);
     float* s_x = reinterpret_cast<float*>(s_ml);  // a row's power of two, until the parts need the place
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int r = t * 8 + quad;
-      const int i = r / p.group, g = r - i * p.group;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (long long)(u.s.q0 + i) * p.qt +
-                                 (long long)(hk * p.group + g) * p.qh;
-      const bool live = r < u.rows;
-      uint32_t w[D / 8];  // this lane's D / 4 elements, in pairs
+      uint32_t (&w)[D / 8] = qw[t];
       if constexpr (F16) {
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (live) x = *reinterpret_cast<const uint4*>(src + c * (D / 4) + k * 8);
-          w[4 * k] = x.x; w[4 * k + 1] = x.y; w[4 * k + 2] = x.z; w[4 * k + 3] = x.w;
-        }
         float top = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 8; ++k)
@@ -403,16 +414,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, NT>::kCtas)) paged_decod
         // 2^k with top 2^k in [2^14, 2^15), k within what a float holds
         const int ex = top > 0.f && top < INFINITY ? min(126, max(-126, 141 - (int)(__float_as_uint(top) >> 23))) : 0;
         const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
-        if (c == 0) s_x[warp * C::kRows + r] = __uint_as_float((uint32_t)(127 - ex) << 23);
+        if (c == 0) s_x[warp * C::kRows + t * 8 + quad] = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
           const __half2 hh = __floats2half2_rn(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
           memcpy(&w[k], &hh, 4);
         }
-      } else {
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k)
-          w[k] = live ? __ldg(reinterpret_cast<const unsigned int*>(src + 16 * (k >> 1) + 8 * (k & 1) + 2 * c)) : 0u;
       }
       // pairs 2s and 2s + 1 are b0 and b1 of k-step s
 #pragma unroll
@@ -740,33 +747,41 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, NT>::kCtas)) paged_decod
 }
 
 // Adds the parts of every unit that several CTAs share: O = sum 2^(m_i - M) O_i
-// over sum 2^(m_i - M) l_i, in the order of the tiles.  One block per unit; a
-// part's (m, l) and O are loaded together, and the running max of a few parts at
-// a time keeps their loads apart from one another.
+// over sum 2^(m_i - M) l_i.  One block per unit, latency-bound: each of its warp
+// groups takes every kMergeGroups-th part, loads a part's (m, l) and O together
+// and a few parts at a time, and the groups' sums are added in order.
+constexpr int kMergeGroups = 4;
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) paged_merge_kernel(const __grid_constant__ DecodeArgs a, float shift) {
+__global__ void __launch_bounds__(kMergeGroups * kThreads) paged_merge_kernel(const __grid_constant__ DecodeArgs a,
+                                                                             float shift) {
+  __shared__ float4 s_acc[kMergeGroups][kThreads];
+  __shared__ float2 s_ml[kMergeGroups][kThreads];
   const PagedParams& p = a.p;
   const int b = blockIdx.x / p.c.Hkv, hk = blockIdx.x - b * p.c.Hkv;
+  const int group = threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
   grid_dep_wait();
   grid_dep_launch();
   const int4 w = a.ws_unit[blockIdx.x];
   const Seq s = seq_of(p.s, p.c, b, p.err);
   const int c0 = w.x, c1 = w.y;
   if (c0 == c1) return;
-  for (int i = threadIdx.x; i < s.n * p.group * (D / 4); i += kThreads) {
+  const int items = s.n * p.group * (D / 4);
+  for (int i0 = 0; i0 < items; i0 += kThreads) {
+    const int i = min(i0 + tid, items - 1);
     const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
     float top = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kAtOnce = 6;
-    for (int q0 = c0; q0 <= c1; q0 += kAtOnce) {
+    constexpr int kAtOnce = 4;
+    for (int q0 = c0 + group; q0 <= c1; q0 += kAtOnce * kMergeGroups) {
       float2 ml[kAtOnce];
       float4 y[kAtOnce];
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
-        const long long at = (2LL * min(q0 + k, c1) + (q0 + k == c0 ? w.z : 0)) * ROWS + r;
+        const int q = q0 + k * kMergeGroups;
+        const long long at = (2LL * min(q, c1) + (min(q, c1) == c0 ? w.z : 0)) * ROWS + r;
         ml[k] = a.ws_ml[at];
         y[k] = *reinterpret_cast<const float4*>(a.ws_o + at * D + x);
-        if (q0 + k > c1) ml[k].x = -INFINITY;
+        if (q > c1) ml[k] = make_float2(-INFINITY, 0.f);
       }
       float m = top;
 #pragma unroll
@@ -777,21 +792,44 @@ __global__ void __launch_bounds__(kThreads) paged_merge_kernel(const __grid_cons
       acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
+        // a part whose rows saw no key has l = 0 and O = 0 (or NaN, which passes on)
         const float f = ml[k].x == -INFINITY ? 0.f : ex2_approx(ml[k].x - m);
-        den = fmaf(f, ml[k].x == -INFINITY ? 0.f : ml[k].y, den);
-        acc.x = fmaf(f, y[k].x, acc.x); acc.y = fmaf(f, y[k].y, acc.y);
-        acc.z = fmaf(f, y[k].z, acc.z); acc.w = fmaf(f, y[k].w, acc.w);
+        den = fmaf(f, ml[k].y, den);
+        if (q0 + k * kMergeGroups <= c1) {
+          acc.x = fmaf(f, y[k].x, acc.x); acc.y = fmaf(f, y[k].y, acc.y);
+          acc.z = fmaf(f, y[k].z, acc.z); acc.w = fmaf(f, y[k].w, acc.w);
+        }
       }
     }
-    const int tok = r / p.group, h = hk * p.group + r - tok * p.group;
-    const float inv = den > 0.f ? 1.f / den : 0.f;
-    uint2 y;
-    y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-    y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (long long)(s.q0 + tok) * p.ot + (long long)h * p.oh;
-    *reinterpret_cast<uint2*>(dst + x) = y;
-    if (x == 0 && p.lse)
-      p.lse[(long long)(s.q0 + tok) * p.Hq + h] = den > 0.f ? (top - shift) * kLn2 + logf(den) : -INFINITY;
+    s_acc[group][tid] = acc;
+    s_ml[group][tid] = make_float2(top, den);
+    __syncthreads();
+    if (group == 0 && i0 + tid < items) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kMergeGroups; ++k) m = fmaxf(m, s_ml[k][tid].x);
+      den = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMergeGroups; ++k) {
+        const float2 ml = s_ml[k][tid];
+        const float4 y = s_acc[k][tid];
+        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+        den = fmaf(f, ml.y, den);
+        acc.x = fmaf(f, y.x, acc.x); acc.y = fmaf(f, y.y, acc.y);
+        acc.z = fmaf(f, y.z, acc.z); acc.w = fmaf(f, y.w, acc.w);
+      }
+      const int tok = r / p.group, h = hk * p.group + r - tok * p.group;
+      const float inv = den > 0.f ? 1.f / den : 0.f;
+      uint2 y;
+      y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+      y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (long long)(s.q0 + tok) * p.ot + (long long)h * p.oh;
+      *reinterpret_cast<uint2*>(dst + x) = y;
+      if (x == 0 && p.lse)
+        p.lse[(long long)(s.q0 + tok) * p.Hq + h] = den > 0.f ? (m - shift) * kLn2 + logf(den) : -INFINITY;
+    }
+    __syncthreads();
   }
 }
 
@@ -817,14 +855,15 @@ cudaError_t decode_one(DecodeArgs& a, bool mod, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_serialized(kern, dim3((unsigned)ctas), dim3(kThreads), (size_t)C::kTotal, stream, a);
   if (e != cudaSuccess || a.whole) return e;
-  return launch_serialized(paged_merge_kernel<D, C::kRows>, dim3((unsigned)(a.p.s.B * a.p.c.Hkv)), dim3(kThreads), 0,
-                           stream, a, kOffset<KV != KV_BF16>);
+  return launch_serialized(paged_merge_kernel<D, C::kRows>, dim3((unsigned)(a.p.s.B * a.p.c.Hkv)),
+                           dim3(kMergeGroups * kThreads), 0, stream, a, kOffset<KV != KV_BF16>);
 }
 template <int KV, int D>
 cudaError_t decode_rows(DecodeArgs& a, bool mod, int ctas, cudaStream_t stream) {
   switch (a.limit) {
     case 8: return decode_one<KV, D, 1>(a, mod, ctas, stream);
     case 16: return decode_one<KV, D, 2>(a, mod, ctas, stream);
+    case 24: return decode_one<KV, D, 3>(a, mod, ctas, stream);
     default: return decode_one<KV, D, 4>(a, mod, ctas, stream);
   }
 }
@@ -833,7 +872,7 @@ cudaError_t decode_rows(DecodeArgs& a, bool mod, int ctas, cudaStream_t stream) 
 // bound max_q gives, at most 32 rows.
 int row_limit(const PagedParams& p) {
   const long long rows = (long long)p.s.max_q * p.group;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : kDecodeRows;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : kDecodeRows;
 }
 
 // One CTA per unit and no merge launch where the caches are so short that
@@ -842,7 +881,7 @@ bool whole_units(const PagedParams& p) { return (long long)p.s.max_pages * p.c.p
 
 // One resident wave.
 int decode_ctas(const PagedParams& p) {
-  return num_sms() * (p.c.dtype != SDPA_CACHE_BF16 && row_limit(p) < 32 ? 3 : 2);
+  return num_sms() * (p.c.dtype != SDPA_CACHE_BF16 && row_limit(p) <= 16 ? 3 : 2);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
