@@ -16,7 +16,6 @@ the formats, the formulas and what the kernels check.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import Optional
@@ -28,9 +27,15 @@ PAGED_PATHS = {"auto": PAGED_AUTO, "exact": PAGED_EXACT, "decode": PAGED_DECODE,
 CACHE_F32, CACHE_BF16, CACHE_E4M3, CACHE_INT8 = 0, 1, 2, 3
 
 
+_package = None
+
+
 def _S():
-    import attention_sdpa_fwd_b200 as S
-    return S
+    global _package
+    if _package is None:
+        import attention_sdpa_fwd_b200 as S
+        _package = S
+    return _package
 
 
 class sdpa_rows_t(ctypes.Structure):
@@ -67,8 +72,11 @@ def bind(L) -> None:
 # ---------------------------------------------------------------------------
 # Raw C-ABI calls (pointers are ints; cache, batch and strides are structures or None)
 # ---------------------------------------------------------------------------
+_byref = ctypes.byref
+
+
 def _ref(x):
-    return None if x is None else ctypes.byref(x)
+    return None if x is None else _byref(x)
 
 
 def sdpa_cache_write(cache, batch, k, k_strides, v, v_strides, dtype, stream) -> int:
@@ -198,36 +206,16 @@ def _rows(t, heads: int, cache: KVCache, name: str) -> Optional[sdpa_rows_t]:
     return sdpa_rows_t(n if t.shape[0] > 1 else max(1, n), h if heads > 1 else max(1, h))
 
 
-@contextlib.contextmanager
-def _switch(device, stream):
-    import torch
-    with torch.cuda.device(device):
-        with torch.cuda.stream(stream):
-            yield (stream or torch.cuda.current_stream(device)).cuda_stream
-
-
-class _Here:
-    """The current stream of the current device, by its handle: asking for the
-    Stream object costs more than the rest of a call's checks."""
-
-    def __enter__(self):
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-
-    def __exit__(self, *exc):
-        return False
-
-
-_here = _Here()
-
-
-def _on(device, stream):
-    """The tensors' device, and the stream asked for, current: what a call
-    allocates belongs to the stream its kernels run on.  Gives the handle."""
+def _on(device, stream, call):
+    """``call(handle)`` with the tensors' device, and the stream asked for,
+    current: what a call allocates belongs to the stream its kernels run on.
+    (By the current stream's handle where nothing has to change: the Stream
+    object alone would cost more than a call's checks.)"""
     import torch
     if stream is None and torch.cuda.current_device() == device.index:
-        return _here
-    return _switch(device, stream)
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return call((stream or torch.cuda.current_stream(device)).cuda_stream)
 
 
 def _check(rc: int, what: str) -> None:
@@ -251,9 +239,8 @@ def cache_write(cache: KVCache, k, v, page_table, kv_lens, cu_q=None, *, max_q: 
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must have one shape and dtype")
     batch = _batch(cache, page_table, kv_lens, cu_q, k.shape[0], max_q)
-    with _on(cache.device, stream) as st:
-        _check(sdpa_cache_write(cache.descriptor(), batch, k.data_ptr(), ks, v.data_ptr(), vs, S._dtype_code(k), st),
-               "sdpa_cache_write")
+    _check(_on(cache.device, stream, lambda st: sdpa_cache_write(
+        cache.descriptor(), batch, k.data_ptr(), ks, v.data_ptr(), vs, S._dtype_code(k), st)), "sdpa_cache_write")
     return cache
 
 
@@ -270,7 +257,9 @@ def cache_read(cache: KVCache, page_table, kv_lens, k_out=None, v_out=None, *, T
     if (k_out is None) != (v_out is None):
         raise ValueError("give both outputs or none")
     batch = _batch(cache, page_table, kv_lens, None, B, None)
-    with _on(cache.device, stream) as st:
+
+    def call(st):
+        nonlocal k_out, v_out, dtype
         if k_out is None:
             if T is None:
                 raise ValueError("cache_read needs T or outputs")
@@ -285,8 +274,9 @@ def cache_read(cache: KVCache, page_table, kv_lens, k_out=None, v_out=None, *, T
         if dtype is not None and dtype != k_out.dtype:
             raise ValueError("dtype differs from the outputs given")
         ks, vs = (None if t.is_contiguous() else _strides(t) for t in (k_out, v_out))
-        _check(sdpa_cache_read(cache.descriptor(), batch, k_out.data_ptr(), ks, v_out.data_ptr(), vs,
-                               S._dtype_code(k_out), k_out.shape[2], st), "sdpa_cache_read")
+        return sdpa_cache_read(cache.descriptor(), batch, k_out.data_ptr(), ks, v_out.data_ptr(), vs,
+                               S._dtype_code(k_out), k_out.shape[2], st)
+    _check(_on(cache.device, stream, call), "sdpa_cache_read")
     return k_out, v_out
 
 
@@ -315,16 +305,18 @@ def sdpa_paged(q, cache: KVCache, page_table, kv_lens, cu_q=None, scale: Optiona
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()
                             or lse.device != dev):
         raise ValueError("lse must be a contiguous float32 [tokens, Hq] tensor on the cache's device")
-    with _on(dev, stream) as st:
+    desc, code, way = cache.descriptor(), S._dtype_code(q), PAGED_PATHS[path]
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+
+    def call(st):
+        nonlocal out
+        os_ = None
         if out is None:
-            out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
-            os_ = None
+            out = torch.empty_like(q) if qs is None else torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
         else:
             if out.shape != q.shape or out.dtype != q.dtype:
                 raise ValueError("out must have q's shape and dtype")
             os_ = _rows(out, Hq, cache, "out")
-        desc, code, way = cache.descriptor(), S._dtype_code(q), PAGED_PATHS[path]
-        scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
         qp, op = q.data_ptr(), out.data_ptr()
         while True:
             have = cache._workspace
@@ -333,12 +325,11 @@ def sdpa_paged(q, cache: KVCache, page_table, kv_lens, cu_q=None, scale: Optiona
                                 None if slopes is None else slopes.data_ptr(), None if lse is None else lse.data_ptr(),
                                 way, None if ws is None else ws.data_ptr(), have, st)
             if rc != -6:
-                break
+                return rc
             # more scratch than the last call on this cache took
             need = sdpa_fwd_paged_workspace(desc, batch, qp, qs, op, os_, code, Hq, way)
-            _check(min(need, 0), "sdpa_fwd_paged_workspace")
             if need <= have:
-                break
+                return int(min(need, -6))
             cache._workspace = need
-        _check(rc, "sdpa_fwd_paged")
+    _check(_on(dev, stream, call), "sdpa_fwd_paged")
     return out
