@@ -339,18 +339,16 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
                         in_page(box_key(key0)), u.hk, page);
           ++r_issued;
         };
-        int pg[2], pv[2] = {0, 0};
+        int pg[2];
         for (int x = 0; x < 2; ++x) pg[x] = page_at(box_key(j_begin * BN + x * kHalf));
-        for (int jj = 0; jj <= n_tiles && ok; ++jj) {
+        for (int jj = 0; jj < n_tiles && ok; ++jj) {
           const int key0 = (j_begin + jj) * BN;
           int nx[2] = {0, 0};
           if (jj + 1 < n_tiles)
             for (int x = 0; x < 2; ++x) nx[x] = page_at(box_key(key0 + BN + x * kHalf));
-          if (jj < n_tiles)
-            for (int x = 0; x < 2 && ok; ++x) load(false, key0 + x * kHalf, pg[x]);
-          if (jj > 0)
-            for (int x = 0; x < 2 && ok; ++x) load(true, key0 - BN + x * kHalf, pv[x]);
-          for (int x = 0; x < 2; ++x) { pv[x] = pg[x]; pg[x] = nx[x]; }
+          for (int y = 0; y < 4 && ok; ++y) load(y >= 2, key0 + (y & 1) * kHalf, y & 1 ? pg[1] : pg[0]);
+          pg[0] = nx[0];
+          pg[1] = nx[1];
         }
         if (!ok) {
           mbar_wait(q_full, 0, nullptr, p.err);
@@ -514,23 +512,21 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
       fetch_page(0);
       fetch_scales(0);
       fetch_page(1);
-      uint32_t v_prev = 0, v_now = 0;  // V's scales of the last two tiles
-      // K(0), then K(j + 1) and V(j) in turn, in one rolled loop: unrolled twice
-      // over, this code and the softmax warps' do not fit the instruction cache
-      // together (2048 new tokens behind 6144, e4m3: 519 us, rolled 313)
+      uint32_t v_scale = 0;
+      // K(j) and V(j) in turn, in one rolled loop: unrolled twice over, this
+      // code and the softmax warps' do not fit the instruction cache together
+      // (2048 new tokens behind 6144, e4m3: 519 us, rolled 313)
 #pragma unroll 1
       for (int it = 0; it < 2 * n_tiles && ok; ++it) {
-        const bool is_v = it == 2 * n_tiles - 1 || (it > 0 && !(it & 1));
-        const int jj = is_v ? (it - 1) >> 1 : (it + 1) >> 1;
-        const int s = jj % NS, use = jj / NS;
-        uint32_t scales = v_prev;
+        const bool is_v = it & 1;
+        const int jj = it >> 1, s = jj % NS, use = jj / NS;
+        uint32_t scales = v_scale;
         if (use > 0) ok = wait_all(mbar_wait(is_v ? &v_empty[s] : &k_empty[s], (use - 1) & 1, abort_v, p.err));
         if (!ok) break;
         if (!is_v) {
           const int ek = common(ks_n), ev = common(vs_n);
           scales = two_halves(ks_n, ek);
-          v_prev = v_now;
-          v_now = two_halves(vs_n, ev);
+          v_scale = two_halves(vs_n, ev);
           // The tile that used this slot, jj - SR, is behind every softmax
           // warp: K stage jj % NS being free means S(jj - NS) is complete, and
           // that S is only issued once tile jj - NS - 1's scores (head_dim 64)
@@ -543,8 +539,6 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
           }
           fetch_scales(jj + 1);
           fetch_page(jj + 2);
-        } else if (jj == n_tiles - 1) {
-          scales = v_now;
         }
         const int rs = r_next % NR;
         ok = wait_all(mbar_wait(&raw_full[rs], (r_next / NR) & 1, abort_v, p.err));
