@@ -43,7 +43,8 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int t, int lane) {
 // an ulp, and q + fl(x - q s) r, both fused, is the correctly rounded quotient
 // unless s's significand is all ones (Markstein, "Computation of elementary
 // functions on the IBM RISC System/6000 processor", 1990).  Three operations
-// an element; a division each had taken the write of a long prompt from TODO.
+// an element where a division is tens (8190 tokens of 12 heads to int8: 20 us
+// for the launch, 33 with divisions and an index computation per piece).
 // r = 0 asks for the division: all-ones significands, and scales so large that
 // r or the remainder could leave the normal range.  (Small x can make the
 // remainder inexact only where the code is 0 either way: s >= 2^-30.)

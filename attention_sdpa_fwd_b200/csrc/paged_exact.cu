@@ -12,29 +12,36 @@
 // once at the end.  Latency-bound on short caches (one round trip per kAhead
 // keys of a group), else bound by re-reading K and V for every query row: this
 // is the fp32 path and the path of layouts the others do not take.
+#include <cooperative_groups.h>
+#include <math.h>
+
 #include "paged.cuh"
 #include "pdl_launch.cuh"
 
 namespace sdpa {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <typename T, typename C, int D>
+constexpr int kWarps = 8;
+constexpr int kAhead = 4;  // keys of a lane group in flight
+
+// kSplit: CTAs of a cluster that share a row's keys; the first adds their sums
+// through distributed shared memory.
+template <typename T, typename C, int D, int kSplit>
 __global__ void __launch_bounds__(kWarps * 32) paged_exact_kernel(const __grid_constant__ PagedParams p, int vec) {
   constexpr int E = 16 / sizeof(C);
   constexpr int G = D / E;  // lanes of a key row
   constexpr int KW = 32 / G;  // key rows of a warp side by side
-  constexpr int kAhead = 4;
   __shared__ float s_acc[kWarps][D];
   __shared__ float s_m[kWarps], s_l[kWarps];
+  __shared__ float s_num[D], s_top, s_den;
   __shared__ int s_b;
   sm100::grid_dep_launch();
   sm100::grid_dep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x, h = blockIdx.y;
+  const int t = blockIdx.x / kSplit, rank = blockIdx.x % kSplit, h = blockIdx.y;
   int b = t;
   if (p.s.cu_q != nullptr) {
     if (threadIdx.x == 0) {
@@ -68,7 +75,18 @@ __global__ void __launch_bounds__(kWarps * 32) paged_exact_kernel(const __grid_c
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) acc[i] = 0.f;
-  for (int j0 = lo + warp * KW * kAhead; j0 < hi; j0 += kWarps * KW * kAhead) {
+  constexpr int kStride = kSplit * kWarps * KW * kAhead;
+  const int first = lo + (rank * kWarps + warp) * KW * kAhead;
+  int entry[kAhead];  // of the next keys, on their way while the last are worked on
+  auto fetch = [&](int j0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int j = j0 + u * KW + lane / G;
+      entry[u] = j < hi ? page_entry(p.s, p.c, b, j) : 0;
+    }
+  };
+  fetch(first);
+  for (int j0 = first; j0 < hi; j0 += kStride) {
     alignas(16) C kr[kAhead][E], vr[kAhead][E];
     float x[kAhead], vscale[kAhead];
 #pragma unroll
@@ -79,7 +97,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_exact_kernel(const __grid_c
 #pragma unroll
       for (int i = 0; i < E; ++i) kr[u][i] = vr[u][i] = C();
       if (j < hi) {
-        const long long page = page_of(p.s, p.c, b, j, p.err);
+        const long long page = max(0, good_page(p.c, entry[u], p.err));
         const int off = j - (int)fdiv((uint32_t)j, p.c.fd_page) * p.c.page_size;
         const C* kp = kb + page * p.c.kp + off * p.c.kt;
         const C* vp = vb + page * p.c.vp + off * p.c.vt;
@@ -98,6 +116,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_exact_kernel(const __grid_c
         }
       }
     }
+    fetch(j0 + kStride);
     float top = m;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -147,6 +166,11 @@ __global__ void __launch_bounds__(kWarps * 32) paged_exact_kernel(const __grid_c
   }
   if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
   __syncthreads();
+  auto finish = [&](float top, float num, float den) {  // column threadIdx.x of the row
+    static_cast<T*>(p.out)[t * p.ot + h * p.oh + threadIdx.x] = from_f32<T>(den > 0.f ? num / den : 0.f);
+    if (p.lse != nullptr && threadIdx.x == 0)
+      p.lse[(long long)t * p.Hq + h] = den > 0.f ? top * kLn2 + logf(den) : -INFINITY;
+  };
   if (threadIdx.x < D) {
     float top = -INFINITY, den = 0.f, num = 0.f;
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
@@ -156,9 +180,33 @@ __global__ void __launch_bounds__(kWarps * 32) paged_exact_kernel(const __grid_c
         den = fmaf(a, s_l[w], den);
         num = fmaf(a, s_acc[w][threadIdx.x], num);
       }
-    static_cast<T*>(p.out)[t * p.ot + h * p.oh + threadIdx.x] = from_f32<T>(den > 0.f ? num / den : 0.f);
-    if (p.lse != nullptr && threadIdx.x == 0)
-      p.lse[(long long)t * p.Hq + h] = den > 0.f ? top * kLn2 + logf(den) : -INFINITY;
+    if constexpr (kSplit > 1) {
+      s_num[threadIdx.x] = num;
+      if (threadIdx.x == 0) { s_top = top; s_den = den; }
+    } else {
+      finish(top, num, den);
+    }
+  }
+  if constexpr (kSplit > 1) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    if (rank == 0 && threadIdx.x < D) {
+      float tops[kSplit], top = -INFINITY, den = 0.f, num = 0.f;
+#pragma unroll
+      for (int r = 0; r < kSplit; ++r) {
+        tops[r] = *cluster.map_shared_rank(&s_top, r);
+        top = fmaxf(top, tops[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < kSplit; ++r) {
+        const float a = top == -INFINITY ? 0.f : exp2f(tops[r] - top);
+        den = fmaf(a, *cluster.map_shared_rank(&s_den, r), den);
+        num = fmaf(a, cluster.map_shared_rank(s_num, r)[threadIdx.x], num);
+      }
+      finish(top, num, den);
+    }
+    cluster.sync();  // the others' shared memory stays until it has been read
   }
 }
 
@@ -168,8 +216,25 @@ cudaError_t exact_one(const PagedParams& p, cudaStream_t stream) {
   const long long es = sizeof(C);
   const bool vec = (reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) | (c.kp * es) | (c.kh * es) |
                     (c.kt * es) | (c.vp * es) | (c.vh * es) | (c.vt * es)) % 16 == 0;
-  return launch_serialized(paged_exact_kernel<T, C, D>, dim3((unsigned)p.s.total_q, (unsigned)p.Hq), dim3(kWarps * 32),
-                           0, stream, p, (int)vec);
+  // Fewer rows than SMs: four CTAs, a cluster, share a row's keys (48 rows of
+  // 1024 keys, f32: 12.5 us against 20.6, graph replay).
+  if ((long long)p.s.total_q * p.Hq <= num_sms()) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.s.total_q * 4, (unsigned)p.Hq);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 4;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, paged_exact_kernel<T, C, D, 4>, p, (int)vec);
+  }
+  return launch_serialized(paged_exact_kernel<T, C, D, 1>, dim3((unsigned)p.s.total_q, (unsigned)p.Hq),
+                           dim3(kWarps * 32), 0, stream, p, (int)vec);
 }
 template <typename T, typename C>
 cudaError_t exact_d(const PagedParams& p, cudaStream_t stream) {
