@@ -11,6 +11,8 @@ namespace sdpa {
 namespace {
 
 constexpr long long kMaxStride = 1LL << 40;
+// tokens of a sequence and rows of a batch: positions less a window stay inside 32 bits
+constexpr long long kMaxTokens = 1LL << 30;
 
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t cache_esz(int dtype) { return dtype == SDPA_CACHE_F32 ? 4 : dtype == SDPA_CACHE_BF16 ? 2 : 1; }
@@ -66,7 +68,7 @@ int check_cache(const sdpa_cache_t* c, CacheView* v) {
 int check_batch(const sdpa_batch_t* s, const CacheView& c, bool rows, BatchView* v) {
   if (s == nullptr) return SDPA_ERR_INVALID_ARG;
   if (s->B < 0 || s->max_pages < 0 || s->table_stride < s->max_pages) return SDPA_ERR_INVALID_ARG;
-  if ((long long)s->max_pages * c.page_size > 0x7fffffffLL - 4096) return SDPA_ERR_UNSUPPORTED;
+  if ((long long)s->max_pages * c.page_size > kMaxTokens) return SDPA_ERR_UNSUPPORTED;
   if (s->B > 0 && s->kv_lens == nullptr) return SDPA_ERR_INVALID_ARG;
   if (s->B > 0 && s->max_pages > 0 && s->page_table == nullptr) return SDPA_ERR_INVALID_ARG;
   if (!aligned_to(s->page_table, 4) || !aligned_to(s->kv_lens, 4) || !aligned_to(s->cu_q, 4)) return SDPA_ERR_MISALIGNED;
@@ -75,6 +77,7 @@ int check_batch(const sdpa_batch_t* s, const CacheView& c, bool rows, BatchView*
   v->kv_lens = s->kv_lens; v->B = s->B;
   if (rows) {
     if (s->total_q < 0 || s->max_q < 0) return SDPA_ERR_INVALID_ARG;
+    if (s->total_q > kMaxTokens) return SDPA_ERR_UNSUPPORTED;
     if (s->cu_q == nullptr && s->total_q != s->B) return SDPA_ERR_INVALID_ARG;
     if (s->B == 0 && s->total_q > 0) return SDPA_ERR_INVALID_ARG;
     v->cu_q = s->cu_q; v->total_q = s->total_q;
@@ -102,7 +105,9 @@ int build_paged(const void* q, const sdpa_rows_t* qs, const sdpa_cache_t* cache,
   p->q = q; p->out = out; p->lse = lse; p->slopes = slopes;
   p->qt = a.t; p->qh = a.h; p->ot = o.t; p->oh = o.h;
   p->Hq = Hq; p->group = Hq / p->c.Hkv;
-  p->scale = scale; p->softcap = softcap; p->window = window;
+  p->scale = scale; p->softcap = softcap;
+  // a window that no sequence of the table can leave is none
+  p->window = window >= (long long)p->s.max_pages * p->c.page_size ? 0 : window;
   const int T = p->s.total_q;
   if (T == 0) return SDPA_OK;
   if (q == nullptr || out == nullptr) return SDPA_ERR_INVALID_ARG;

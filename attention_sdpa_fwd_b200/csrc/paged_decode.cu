@@ -180,7 +180,7 @@ __device__ __forceinline__ uint32_t v_off(int key, int piece) {
 
 struct Unit {
   Seq s;
-  int rows;      // n * group
+  int rows;      // n * group, 0 if they are too many for this kernel
   int lo16, hi;  // first key (rounded down to 16) and end of what any row sees
   int lo;
   int nt;        // tiles
@@ -190,11 +190,11 @@ template <int TK>
 __device__ __forceinline__ Unit unit_of(const DecodeArgs& a, int b) {
   Unit u;
   u.s = seq_of(a.p.s, a.p.c, b, a.p.err);
-  u.rows = u.s.n * a.p.group;
+  u.rows = u.s.n <= a.limit / a.p.group ? u.s.n * a.p.group : 0;  // 0: none, or not this kernel's
   u.hi = u.s.L;
   u.lo = a.p.window > 0 ? max(0, u.s.L - u.s.n + 1 - a.p.window) : 0;
   u.lo16 = u.lo & ~15;
-  u.nt = u.rows > 0 && u.rows <= a.limit && u.hi > u.lo ? (u.hi - u.lo16 + TK - 1) / TK : 0;
+  u.nt = u.rows > 0 && u.hi > u.lo ? (u.hi - u.lo16 + TK - 1) / TK : 0;
   return u;
 }
 
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, NT>::kCtas)) paged_decod
     const Unit u = unit_of<C::kKeys>(a, bb);
     if (u.nt != 0) continue;
     if (!a.whole && tid == 0) a.ws_unit[unit] = make_int4(0, 0, 0, 0);
-    if (u.rows == 0 || u.rows > a.limit) continue;
+    if (u.rows == 0) continue;
     for (int i = tid; i < u.rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
       const int tok = r / p.group, h = hk * p.group + r - tok * p.group;

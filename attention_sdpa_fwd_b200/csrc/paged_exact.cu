@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_exact_kernel(const __grid_c
   }
   const Seq q = seq_of(p.s, p.c, b, p.err);
   if (t < q.q0 || t >= q.q0 + q.n) return;  // a row behind the last sequence: left as it is
-  if (q.n * p.group <= p.skip_rows) return;
+  if (q.n <= p.skip_rows / p.group) return;
   const int pos = q.L - q.n + (t - q.q0);
   int lo, hi;
   seen(p, pos, lo, hi);

@@ -107,7 +107,7 @@ struct TcUnit {
 
 __device__ __forceinline__ int blocks_of(const TcPagedArgs& a, int b) {
   const Seq s = seq_of(a.p.s, a.p.c, b, a.p.err);
-  if (s.n * a.p.group <= a.limit) return 0;
+  if (s.n <= a.limit / a.p.group) return 0;
   return (s.n + 2 * a.tok - 1) / (2 * a.tok);
 }
 
@@ -652,7 +652,10 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
         mbar_arrive(q_ready);
       }
     }
-    const uint64_t xs2 = f2(xs, xs);
+    // MOD 0 multiplies masked scores, -inf, by the factor as well: it must not
+    // become 0 (below 2^-119 every score is as good as 0 anyway)
+    auto at_least = [](float x) { return MOD == 0 ? fmaxf(x, 1.5e-36f) : x; };
+    const uint64_t xs2 = f2(at_least(xs), at_least(xs));
     const float slope = MOD && p.slopes && row_valid ? __ldg(p.slopes + h) * kLog2e : 0.f;
     const float cap_in = MOD == 2 ? 2.f / p.softcap : 0.f;  // of scores in log2 units
     const float cap_out = p.softcap * kLog2e;
@@ -685,7 +688,8 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
 #pragma unroll
         for (int y = 0; y < NG; ++y) {
           const float4 e = sSc[(jj % SR) * 4 + y];
-          gx2[y] = f2(xs * e.x, xs * e.x);
+          const float gx = at_least(xs * e.x);
+          gx2[y] = f2(gx, gx);
           goff[y] += e.y;
           gsum[y] = e.z;
         }

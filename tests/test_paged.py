@@ -290,6 +290,28 @@ def test_bad_device_values_are_reported(path, kw):
     assert bad_batch(path) == 0
 
 
+@pytest.mark.parametrize("cdt", [BF16, E4M3, INT8])
+@pytest.mark.parametrize("path", ["decode", "tcgen05"])
+def test_tiny_and_huge_rows(path, cdt):
+    """Rows of q at the ends of the range, an all-zero one, a tiny scale, masked
+    keys beside them; a window no sequence can leave, and the largest."""
+    pool = R.Pool(cdt, 2, 64, 16, [70, 140], seed=11)
+    n = [3, 2]
+    q = torch.randn(5, 8, 64, generator=torch.Generator().manual_seed(5))
+    q[0] *= 1e-37
+    q[1] = 0
+    q[2] *= 3e4
+    q = q.to(BF16)
+    codes = cdt in R.QMAX
+    for kw in (dict(), dict(scale=1e-38), dict(window=2 ** 31 - 1), dict(window=140), dict(window=139)):
+        out = S.sdpa_paged(q.cuda(), pool.cache(), pool.table.cuda(), pool.lens.cuda(), cu(n), max_q=3, path=path, **kw)
+        assert device_error() == 0
+        want, _, tol, _ = R.attend(pool, q, n, u_p=R.U[torch.float16 if codes else BF16],
+                                   p_floor=2.0 ** -37 if codes else 0.0,
+                                   u_kv=R.U[torch.float16] if codes and path == "tcgen05" else 0.0, **kw)
+        R.check(out, want, tol, BF16, f"{path} {cdt} {kw}")
+
+
 def test_entries_past_the_tokens_are_not_read():
     """Table entries behind a sequence's tokens, and in front of its window, may be anything."""
     for path in ("exact", "decode", "tcgen05"):

@@ -60,7 +60,7 @@ BAD_CACHES = [(dict(dtype=4), -1), (dict(dtype=-1), -1), (dict(d=32), -2), (dict
 BAD_BATCHES = [(dict(B=-1), -1), (dict(max_pages=-1), -1), (dict(table_stride=3), -1), (dict(kv_lens=None), -1),
                (dict(page_table=None), -1), (dict(page_table=TAB + 2), -3), (dict(kv_lens=LEN + 1), -3),
                (dict(max_pages=1 << 28, table_stride=1 << 28), -2)]
-BAD_ROWS = [(dict(total_q=-1), -1), (dict(max_q=-1), -1), (dict(cu_q=None), -1), (dict(B=0), -1), (dict(cu_q=CU + 1), -3)]
+BAD_ROWS = [(dict(total_q=(1 << 30) + 1), -2), (dict(total_q=-1), -1), (dict(max_q=-1), -1), (dict(cu_q=None), -1), (dict(B=0), -1), (dict(cu_q=CU + 1), -3)]
 
 
 @pytest.mark.parametrize("call", [paged, write, read])
