@@ -40,6 +40,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "paged.cuh"
@@ -875,14 +876,22 @@ int row_limit(const PagedParams& p) {
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : kDecodeRows;
 }
 
-// One CTA per unit and no merge launch where the caches are so short that
-// splitting them would cost more than it gives (a sequence of 131 tokens: 8.5 us
-// against 12.4 with the second launch, graph replay).
-bool whole_units(const PagedParams& p) { return (long long)p.s.max_pages * p.c.page_size <= 512; }
-
 // One resident wave.
 int decode_ctas(const PagedParams& p) {
   return num_sms() * (p.c.dtype != SDPA_CACHE_BF16 && row_limit(p) <= 16 ? 3 : 2);
+}
+
+// One CTA per unit and no merge launch where splitting the keys would cost more
+// than it gives: where no sequence reaches past 512 keys (one of 131 tokens: 8.5
+// us against 12.4, graph replay), and, with a unit for every SM, past 1088 (32
+// sequences of up to 1024, bf16: 17.9 against 22.0; 24 with drafts, e4m3: 26.7
+// against 43.7; a window of 1024: 18.7 against 22.8), or past 2176 while all
+// units are resident at once (32 of up to 2048, bf16: 37.6 against 41.3; beyond
+// one wave the tail costs more: 64 of up to 2048, e4m3: 63.8 against 56.0).
+bool whole_units(const PagedParams& p) {
+  const long long cap = (long long)p.s.max_pages * p.c.page_size, units = (long long)p.s.B * p.c.Hkv;
+  const long long reach = p.window > 0 ? std::min(cap, (long long)p.window + p.s.max_q + 16) : cap;
+  return reach <= 512 || (units >= num_sms() && reach <= (units <= decode_ctas(p) ? 2176 : 1088));
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }

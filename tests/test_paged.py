@@ -537,3 +537,11 @@ def test_large_offsets():
     for a, b in (outs, one):
         assert (a.float() - b.float()).abs().max() < 2.0 ** -5 and (a.float() - b.float()).abs().mean() < 2.0 ** -9
     assert torch.isfinite(outs[0]).all()
+
+
+@pytest.mark.parametrize("cdt", [BF16, E4M3, INT8])
+def test_decode_whole_units(cdt):
+    """A unit for every SM and short reaches: no unit is split (a window inside long caches, drafts)."""
+    run_case("decode", cdt, BF16, 32, 16, 64, 16, [900] * 5 + [0, 1, 33, 2000, 64], None, window=300)
+    run_case("decode", cdt, BF16, 16, 16, 128, 32, [(97 * i) % 700 for i in range(10)],
+             [min(4, (97 * i) % 700) for i in range(10)])
