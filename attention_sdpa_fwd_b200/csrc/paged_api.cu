@@ -254,10 +254,11 @@ extern "C" int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const
 
 extern "C" int64_t sdpa_fwd_paged_workspace(const sdpa_cache_t* cache, const sdpa_batch_t* batch, const void* q,
                                             const sdpa_rows_t* q_strides, const void* out,
-                                            const sdpa_rows_t* out_strides, sdpa_dtype_t dtype, int Hq, int path) {
+                                            const sdpa_rows_t* out_strides, sdpa_dtype_t dtype, int Hq, int window,
+                                            int path) {
   if (path < SDPA_PAGED_AUTO || path > SDPA_PAGED_TCGEN05) return SDPA_ERR_INVALID_ARG;
   PagedParams p;
-  const int rc = build_paged(q, q_strides, cache, batch, const_cast<void*>(out), out_strides, dtype, Hq, 1.f, 0, 0.f,
+  const int rc = build_paged(q, q_strides, cache, batch, const_cast<void*>(out), out_strides, dtype, Hq, 1.f, window, 0.f,
                              nullptr, nullptr, &p);
   if (rc != SDPA_OK) return rc;
   if (p.s.total_q == 0) return 0;

@@ -1,16 +1,16 @@
-// Attention over a paged cache for sequences with few new rows: at most 16 or
-// 32 (token, head) rows share a kv head (one new token, or a few drafted ones).
+// Attention over a paged cache for sequences with few new rows: at most 32
+// (token, head) rows share a kv head (one new token, or a few drafted ones).
 //
 // HBM-bound: every key and value of the batch is read once, 4 d operations per
 // (row, key) are far below what the bytes leave room for.  So the work is laid
 // out by bytes, not by sequences:
 //
-//  * Work is counted in tiles of KS keys per stream of one (sequence, kv head),
-//    all units in one row; CTA c of G takes tiles [T c / G, T (c+1) / G), T from
+//  * Work is counted in tiles, a step of KS keys for each of a CTA's warps, of
+//    one (sequence, kv head), all of these units in one row; CTA c of G takes tiles [T c / G, T (c+1) / G), T from
 //    a scan of the lengths at its start.  Every CTA streams the same number of
 //    bytes whatever the lengths are.  A unit that ends up in several CTAs
 //    leaves unnormalised parts (O, max, sum) in the workspace, at most two per
-//    CTA, and merge_kernel, launched behind, adds them in a fixed order: no
+//    CTA, and paged_merge_kernel, launched behind, adds them in a fixed order: no
 //    atomics, no state between calls.
 //  * Each warp runs on its own: it copies KS keys and values at a time with
 //    16-byte cp.async into its own ring of NST stages and never waits for
@@ -908,7 +908,7 @@ int paged_decode_check(const PagedParams& p, sdpa_dtype_t dtype) {
   for (long long x : bytes)
     if (x % 16 != 0) return SDPA_ERR_MISALIGNED;
   // strides of a page, and offsets inside one, in 32 bits
-  const long long wide[] = {c.kp * es, c.vp * es, c.kt * es * c.page_size, c.vt * es * c.page_size, c.ksp, c.vsp,
+  const long long wide[] = {c.kp * es, c.vp * es, c.kt * es, c.vt * es, c.kst, c.vst, c.kt * es * c.page_size, c.vt * es * c.page_size, c.ksp, c.vsp,
                             c.kst * c.page_size, c.vst * c.page_size};
   for (long long x : wide)
     if (x > 0x7fffffffLL) return SDPA_ERR_UNSUPPORTED;

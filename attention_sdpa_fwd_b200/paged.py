@@ -63,7 +63,7 @@ def bind(L) -> None:
     L.sdpa_cache_write.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp]
     L.sdpa_cache_read.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp]
     L.sdpa_fwd_paged.argtypes = [_vp] * 6 + [_i32, _i32, _f32, _i32, _f32, _vp, _vp, _i32, _vp, _i64, _vp]
-    L.sdpa_fwd_paged_workspace.argtypes = [_vp] * 6 + [_i32, _i32, _i32]
+    L.sdpa_fwd_paged_workspace.argtypes = [_vp] * 6 + [_i32] * 4
     for n in ("sdpa_cache_write", "sdpa_cache_read", "sdpa_fwd_paged"):
         getattr(L, n).restype = _i32
     L.sdpa_fwd_paged_workspace.restype = _i64
@@ -94,9 +94,9 @@ def sdpa_fwd_paged(q, q_strides, cache, batch, out, out_strides, dtype, Hq, scal
                                      scale, window, softcap, slopes, lse, path, workspace, workspace_bytes, stream)
 
 
-def sdpa_fwd_paged_workspace(cache, batch, q, q_strides, out, out_strides, dtype, Hq, path) -> int:
+def sdpa_fwd_paged_workspace(cache, batch, q, q_strides, out, out_strides, dtype, Hq, window, path) -> int:
     return _S().lib().sdpa_fwd_paged_workspace(_ref(cache), _ref(batch), q, _ref(q_strides), out, _ref(out_strides),
-                                               dtype, Hq, path)
+                                               dtype, Hq, window, path)
 
 
 # ---------------------------------------------------------------------------
@@ -327,7 +327,7 @@ def sdpa_paged(q, cache: KVCache, page_table, kv_lens, cu_q=None, scale: Optiona
             if rc != -6:
                 return rc
             # more scratch than the last call on this cache took
-            need = sdpa_fwd_paged_workspace(desc, batch, qp, qs, op, os_, code, Hq, way)
+            need = sdpa_fwd_paged_workspace(desc, batch, qp, qs, op, os_, code, Hq, int(window), way)
             if need <= have:
                 return int(min(need, -6))
             cache._workspace = need

@@ -376,7 +376,8 @@ typedef enum {
   SDPA_PAGED_EXACT = 1,  /* CUDA cores, fp32 arithmetic; every type, layout and option */
   SDPA_PAGED_DECODE = 2, /* few new rows (max_q * Hq / Hkv <= 32): mma.sync, the keys of the whole batch
                             divided evenly over the SMs; BF16 I/O, d 64 or 128, page_size a multiple of
-                            16, 16-byte aligned rows of q and the cache */
+                            16, 16-byte aligned rows of q and the cache, page strides and the extent of
+                            a page's tokens below 2^31 bytes */
   SDPA_PAGED_TCGEN05 = 3 /* chunks: TMA + tcgen05/TMEM tiles of 128 (token, head) rows; BF16 I/O, d 64
                             or 128, Hq / Hkv <= 128, page_size a multiple of 16, 16-byte aligned rows
                             of q, out and the cache */
@@ -415,7 +416,7 @@ int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const sdpa_cache
    call whose arguments differ in the addresses of equally aligned buffers. */
 int64_t sdpa_fwd_paged_workspace(const sdpa_cache_t* cache, const sdpa_batch_t* batch, const void* q,
                                  const sdpa_rows_t* q_strides, const void* out, const sdpa_rows_t* out_strides,
-                                 sdpa_dtype_t dtype, int Hq, int path);
+                                 sdpa_dtype_t dtype, int Hq, int window, int path);
 
 /* Synchronises `stream`, then returns and clears the device error word of the
    current device: SDPA_OK; SDPA_ERR_DEVICE_INDEX when a paged operator met a

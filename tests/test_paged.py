@@ -545,3 +545,10 @@ def test_decode_whole_units(cdt):
     run_case("decode", cdt, BF16, 32, 16, 64, 16, [900] * 5 + [0, 1, 33, 2000, 64], None, window=300)
     run_case("decode", cdt, BF16, 16, 16, 128, 32, [(97 * i) % 700 for i in range(10)],
              [min(4, (97 * i) % 700) for i in range(10)])
+
+
+@pytest.mark.parametrize("window", [1, 200, 600, 1500, 2999, 3000])
+def test_chunk_windows_on_long_tables(window):
+    """How a chunk's keys are split, and the scratch for it, go by the window."""
+    run_case("auto", BF16, BF16, 4, 1, 64, 16, [3000], [200], window=window)
+    run_case("auto", E4M3, BF16, 4, 2, 128, 32, [3000, 900], [40, 1], window=window)

@@ -131,8 +131,8 @@ def test_nothing_to_do():
     assert paged(None, batch(total_q=0)) == 0 and read(T=0, k=None, v=None) == 0
 
 
-def workspace(c=None, b=None, Hq=4, path=0, dtype=BF16):
-    return S.sdpa_fwd_paged_workspace(c or cache(), b or batch(), Q, None, O, None, dtype, Hq, path)
+def workspace(c=None, b=None, Hq=4, path=0, dtype=BF16, window=0):
+    return S.sdpa_fwd_paged_workspace(c or cache(), b or batch(), Q, None, O, None, dtype, Hq, window, path)
 
 
 def test_workspace_sizes():
@@ -141,6 +141,13 @@ def test_workspace_sizes():
     assert workspace(b=long) > 0
     assert workspace(b=long, path=1) == 0 and workspace(b=long, dtype=7) == -1 and workspace(b=long, path=9) == -1
     assert workspace(b=batch(total_q=0)) == 0
+    assert workspace(b=long, window=64) == 0 and workspace(b=long, window=-1) == -1
+    # a window changes how chunks are split: what is asked for is what the call wants
+    for window in (0, 200, 600, 1500, 5000, 9000):
+        b = batch(B=1, max_pages=600, table_stride=600, total_q=200, max_q=200)
+        need = workspace(b=b, window=window)
+        assert paged(None, b, window=window, ws=W, ws_bytes=need - 1) == -6 if need else True
+        assert need >= 0
     # both kernels of a mixed batch have their share
     mixed = batch(max_pages=512, table_stride=512, total_q=400, max_q=300)
     assert workspace(b=mixed) > workspace(b=mixed, path=3) > 0
