@@ -307,6 +307,8 @@ def sdpa_paged(q, cache: KVCache, page_table, kv_lens, cu_q=None, scale: Optiona
         raise ValueError("lse must be a contiguous float32 [tokens, Hq] tensor on the cache's device")
     desc, code, way = cache.descriptor(), S._dtype_code(q), PAGED_PATHS[path]
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    # to the C int's range (ctypes would keep the low bits only); one past every cache is none there too
+    window = min(max(int(window), -1), 0x7fffffff)
 
     def call(st):
         nonlocal out
@@ -321,13 +323,13 @@ def sdpa_paged(q, cache: KVCache, page_table, kv_lens, cu_q=None, scale: Optiona
         while True:
             have = cache._workspace
             ws = torch.empty(have, dtype=torch.uint8, device=dev) if have else None
-            rc = sdpa_fwd_paged(qp, qs, desc, batch, op, os_, code, Hq, scale, int(window), float(softcap),
+            rc = sdpa_fwd_paged(qp, qs, desc, batch, op, os_, code, Hq, scale, window, float(softcap),
                                 None if slopes is None else slopes.data_ptr(), None if lse is None else lse.data_ptr(),
                                 way, None if ws is None else ws.data_ptr(), have, st)
             if rc != -6:
                 return rc
             # more scratch than the last call on this cache took
-            need = sdpa_fwd_paged_workspace(desc, batch, qp, qs, op, os_, code, Hq, int(window), way)
+            need = sdpa_fwd_paged_workspace(desc, batch, qp, qs, op, os_, code, Hq, window, way)
             if need <= have:
                 return int(min(need, -6))
             cache._workspace = need

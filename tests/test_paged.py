@@ -552,3 +552,15 @@ def test_chunk_windows_on_long_tables(window):
     """How a chunk's keys are split, and the scratch for it, go by the window."""
     run_case("auto", BF16, BF16, 4, 1, 64, 16, [3000], [200], window=window)
     run_case("auto", E4M3, BF16, 4, 2, 128, 32, [3000, 900], [40, 1], window=window)
+
+
+def test_window_past_32_bits():
+    """A window wider than a C int is no window, and a negative one is refused whatever its low bits."""
+    pool, q, _, _, table, lens = decode_setup()
+    cache = pool.cache()
+    want = S.sdpa_paged(q, cache, table, lens)
+    for window in (2 ** 31, 2 ** 32 + 1, 2 ** 40):
+        assert torch.equal(S.sdpa_paged(q, cache, table, lens, window=window), want)
+    for window in (-1, -2 ** 32 + 1):
+        with pytest.raises(S.SdpaError):
+            S.sdpa_paged(q, cache, table, lens, window=window)
