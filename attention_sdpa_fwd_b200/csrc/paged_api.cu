@@ -207,6 +207,7 @@ extern "C" int sdpa_cache_read(const sdpa_cache_t* cache, const sdpa_batch_t* ba
   int rc = check_cache(cache, &c);
   if (rc == SDPA_OK) rc = check_batch(batch, c, false, &s);
   if (rc != SDPA_OK) return rc;
+  if (T > kMaxTokens) return SDPA_ERR_UNSUPPORTED;
   if (!is_codes(c.dtype) && (c.dtype == SDPA_CACHE_F32) != (dtype == SDPA_F32)) return SDPA_ERR_UNSUPPORTED;
   const sdpa_strides_t dense = {(int64_t)c.Hkv * T * c.d, (int64_t)T * c.d, c.d};
   const sdpa_strides_t ks = k_strides ? *k_strides : dense, vs = v_strides ? *v_strides : dense;

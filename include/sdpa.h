@@ -311,8 +311,10 @@ int sdpa_fwd_split_kv_static(const void* q, const void* k, const void* v, void* 
  * total_q (cu_q NULL: one row each, total_q == B), at most max_q of them.  The
  * new rows are the sequence's LAST tokens: row i is at position
  * kv_lens[b] - n_b + i.  Rows behind cu_q[B] belong to nobody and are left as
- * they are.  Tables, lengths and cu_q are device memory, read by the kernels
- * in stream order, so a captured call replays with the lengths of the replay.
+ * they are.  max_pages * page_size and total_q (and the T of sdpa_cache_read)
+ * may be up to 2^30, else SDPA_ERR_UNSUPPORTED.  Tables, lengths and cu_q are
+ * device memory, read by the kernels in stream order, so a captured call
+ * replays with the lengths of the replay.
  *
  * What the host cannot check the kernels do, in every build: a page number
  * outside the pool, a length below 0 or past max_pages * page_size, a query

@@ -181,3 +181,10 @@ def test_strides_of_one_element_axes():
     s = _strides(t.as_strided((1, 2, 1, 64), (0, 64, 0, 1)))
     assert (s.b, s.h, s.t) == (1, 64, 1)
     assert ctypes.sizeof(S.sdpa_strides_t) == 24
+
+
+def test_read_refuses_rows_past_the_longest_sequence():
+    one = S.sdpa_strides_t(64, 64, 64)
+    for T in ((1 << 30) + 1, (1 << 31) - 32, (1 << 31) - 1):
+        assert read(cache(Hkv=1), batch(B=1), T=T) == -2
+        assert read(cache(Hkv=1), batch(B=1), ks=one, vs=one, T=T) == -2
