@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, NT>::kCtas)) paged_decod
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int w = 0; w < kWarps; ++w) {
         const float2 ml = s_ml[w * C::kRows + r];
-        if (ml.x != -INFINITY) den = fmaf(ex2_approx(ml.x - top), ml.y, den);
+        den = fmaf(ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top), ml.y, den);
         const float4 y = *reinterpret_cast<const float4*>(mrg + (w * C::kRows + r) * C::kPitch + x);
         acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
       }
@@ -715,14 +715,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, NT>::kCtas)) paged_decod
         if (x == 0) a.ws_ml[slot * C::kRows + r] = make_float2(top, den);
       } else {
         const int tok = r / p.group, h = hk * p.group + r - tok * p.group;
-        const float inv = den > 0.f ? 1.f / den : 0.f;
+        const float inv = den != 0.f ? 1.f / den : 0.f;
         uint2 y;
         y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
         y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (long long)(u.s.q0 + tok) * p.ot + (long long)h * p.oh;
         *reinterpret_cast<uint2*>(dst + x) = y;
         if (x == 0 && p.lse)
-          p.lse[(long long)(u.s.q0 + tok) * p.Hq + h] = den > 0.f ? (top - kShift) * kLn2 + logf(den) : -INFINITY;
+          p.lse[(long long)(u.s.q0 + tok) * p.Hq + h] = den != 0.f ? (top - kShift) * kLn2 + logf(den) : -INFINITY;
       }
     }
     __syncthreads();  // before the next unit's copies land in the ring
@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(kMergeGroups * kThreads) paged_merge_kernel(co
       acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
-        // a part whose rows saw no key has l = 0 and O = 0 (or NaN, which passes on)
+        // a part whose rows saw no key has l = 0 and O = 0; NaN in either passes on
         const float f = ml[k].x == -INFINITY ? 0.f : ex2_approx(ml[k].x - m);
         den = fmaf(f, ml[k].y, den);
         if (q0 + k * kMergeGroups <= c1) {
@@ -821,14 +821,14 @@ __global__ void __launch_bounds__(kMergeGroups * kThreads) paged_merge_kernel(co
         acc.z = fmaf(f, y.z, acc.z); acc.w = fmaf(f, y.w, acc.w);
       }
       const int tok = r / p.group, h = hk * p.group + r - tok * p.group;
-      const float inv = den > 0.f ? 1.f / den : 0.f;
+      const float inv = den != 0.f ? 1.f / den : 0.f;
       uint2 y;
       y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
       y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (long long)(s.q0 + tok) * p.ot + (long long)h * p.oh;
       *reinterpret_cast<uint2*>(dst + x) = y;
       if (x == 0 && p.lse)
-        p.lse[(long long)(s.q0 + tok) * p.Hq + h] = den > 0.f ? (m - shift) * kLn2 + logf(den) : -INFINITY;
+        p.lse[(long long)(s.q0 + tok) * p.Hq + h] = den != 0.f ? (m - shift) * kLn2 + logf(den) : -INFINITY;
     }
     __syncthreads();
   }

@@ -133,21 +133,21 @@ __global__ void __launch_bounds__(kWarps * 32) paged_exact_kernel(const __grid_c
       }
       top = fmaxf(top, x[u]);
     }
-    if (top != -INFINITY) {
-      const float a = exp2f(m - top);
-      l *= a;
+    // the maxima pass over NaN scores, the weights and their sum do not
+    const float from = top == -INFINITY ? 0.f : top;
+    const float a = exp2f(m - from);
+    l *= a;
 #pragma unroll
-      for (int i = 0; i < E; ++i) acc[i] *= a;
+    for (int i = 0; i < E; ++i) acc[i] *= a;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const float w = exp2f(x[u] - top);
-        l += w;
-        const float wv = w * vscale[u];
+    for (int u = 0; u < kAhead; ++u) {
+      const float w = exp2f(x[u] - from);
+      l += w;
+      const float wv = w * vscale[u];
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = fmaf(wv, cache_elem(vr[u][i]), acc[i]);
-      }
-      m = top;
+      for (int i = 0; i < E; ++i) acc[i] = fmaf(wv, cache_elem(vr[u][i]), acc[i]);
     }
+    m = top;
   }
   // lane groups of the warp, then the warps
 #pragma unroll
@@ -167,19 +167,18 @@ __global__ void __launch_bounds__(kWarps * 32) paged_exact_kernel(const __grid_c
   if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
   __syncthreads();
   auto finish = [&](float top, float num, float den) {  // column threadIdx.x of the row
-    static_cast<T*>(p.out)[t * p.ot + h * p.oh + threadIdx.x] = from_f32<T>(den > 0.f ? num / den : 0.f);
+    static_cast<T*>(p.out)[t * p.ot + h * p.oh + threadIdx.x] = from_f32<T>(den != 0.f ? num / den : 0.f);
     if (p.lse != nullptr && threadIdx.x == 0)
-      p.lse[(long long)t * p.Hq + h] = den > 0.f ? top * kLn2 + logf(den) : -INFINITY;
+      p.lse[(long long)t * p.Hq + h] = den != 0.f ? top * kLn2 + logf(den) : -INFINITY;
   };
   if (threadIdx.x < D) {
     float top = -INFINITY, den = 0.f, num = 0.f;
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-    if (top != -INFINITY)
-      for (int w = 0; w < kWarps; ++w) {
-        const float a = exp2f(s_m[w] - top);
-        den = fmaf(a, s_l[w], den);
-        num = fmaf(a, s_acc[w][threadIdx.x], num);
-      }
+    for (int w = 0; w < kWarps; ++w) {
+      const float a = top == -INFINITY ? 0.f : exp2f(s_m[w] - top);
+      den = fmaf(a, s_l[w], den);
+      num = fmaf(a, s_acc[w][threadIdx.x], num);
+    }
     if constexpr (kSplit > 1) {
       s_num[threadIdx.x] = num;
       if (threadIdx.x == 0) { s_top = top; s_den = den; }

@@ -170,17 +170,23 @@ __device__ __forceinline__ bool find_unit(const TcPagedArgs& a, int unit, TcUnit
   return true;
 }
 
+// The smaller, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 // Four scores x in log2 units to c tanh(x / c) = c - 2 c / (1 + 2^(2 x / c)),
 // one reciprocal for the four: 1 / a = b c d / (a b c d).  The exponent is kept
 // below 30, where tanh is 1 - 2^-29, so that the product stays finite.
 // (The multi-function unit bounds capped scores: 2.25 operations a score
-// instead of 3.)
+// instead of 3.)  A NaN reaches all four.
 __device__ __forceinline__ void cap4(uint64_t& x, uint64_t& y, float cap_in, float cap_out) {
   float v[4], a[4];
   f2_split(x, v[0], v[1]);
   f2_split(y, v[2], v[3]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = 1.f + ex2_approx(fminf(v[i] * cap_in, 30.f));
+  for (int i = 0; i < 4; ++i) a[i] = 1.f + ex2_approx(min_nan(v[i] * cap_in, 30.f));
   const float ab = a[0] * a[1], cd = a[2] * a[3];
   const float r = rcp_approx(ab * cd) * (-2.f * cap_out);
   const float rab = r * cd, rcd = r * ab;
@@ -694,6 +700,14 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
           gsum[y] = e.z;
         }
       }
+      const bool edge = !(j0 >= lo_i && j0 + BN <= hi_i);
+      if constexpr (MOD == 2) {
+        if (edge) {  // a masked NaN must not share a visible score's reciprocal
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (j0 + c < lo_i || j0 + c >= hi_i) sr[c] = 0;
+        }
+      }
       // slopes: (j - pos) slope = a group's first key's, in goff, + 0, slope, 2 slope ..
       // over the group, a running sum (32 steps: the fp32 rounding of the scores)
       uint64_t x2[BN / 2];
@@ -719,7 +733,7 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
           if constexpr (MOD == 1) ramp = f2_add(ramp, two);
         }
       }
-      if (!(j0 >= lo_i && j0 + BN <= hi_i)) {
+      if (edge) {
 #pragma unroll
         for (int c = 0; c < BN; ++c)
           if (j0 + c < lo_i || j0 + c >= hi_i) {
@@ -801,16 +815,16 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
       const long long tok = u.s.q0 + i;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + tok * p.ot + (long long)h * p.oh;
       if (live) {
-        tile::store_o_row<D>(o_addr, l_run > 0.f ? 1.f / l_run : 0.f, orow, row_valid);
+        tile::store_o_row<D>(o_addr, l_run != 0.f ? 1.f / l_run : 0.f, orow, row_valid);
       } else if (row_valid && n_tiles == 0) {
 #pragma unroll
         for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(orow + c) = make_uint4(0, 0, 0, 0);
       }
-      if (row_valid && p.lse) p.lse[tok * p.Hq + h] = l_run > 0.f ? m_off * kLn2 + logf(l_run) : -INFINITY;
+      if (row_valid && p.lse) p.lse[tok * p.Hq + h] = l_run != 0.f ? m_off * kLn2 + logf(l_run) : -INFINITY;
     } else {
       const long long part = (long long)unit * args.n_split + sidx;
       const int row = t * kRows + lr;
-      const bool have = live && l_run > 0.f;
+      const bool have = live && l_run != 0.f;
       if (live) {
         float4* wo = reinterpret_cast<float4*>(args.ws_o) + part * (D / 4) * 256 + row;
 #pragma unroll
@@ -869,7 +883,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const __g
     float4 acc[4] = {};
 #pragma unroll
     for (int k = 0; k < kMaxSplit; ++k) {
-      if (ml[k].x == -INFINITY) continue;  // a part without keys wrote nothing else
+      if (ml[k].y == 0.f) continue;  // a part without keys wrote nothing else
       const float w = ex2_approx(ml[k].x - top);
       den = fmaf(w, ml[k].y, den);
       const float4* src = reinterpret_cast<const float4*>(args.ws_o) + ((part0 + k) * (D / 4) + c0) * 256 + row;
@@ -880,7 +894,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const __g
         acc[c].z = fmaf(w, y.z, acc[c].z); acc[c].w = fmaf(w, y.w, acc[c].w);
       }
     }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = den != 0.f ? 1.f / den : 0.f;
     const long long tok = u.s.q0 + i;
     const int h = u.hk * p.group + g;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tok * p.ot + (long long)h * p.oh + c0 * 4;
@@ -893,7 +907,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const __g
       y.w = pack_bf16x2(acc[c + 1].z * inv, acc[c + 1].w * inv);
       *reinterpret_cast<uint4*>(dst + c * 4) = y;
     }
-    if (c0 == 0 && p.lse) p.lse[tok * p.Hq + h] = den > 0.f ? top * kLn2 + logf(den) : -INFINITY;
+    if (c0 == 0 && p.lse) p.lse[tok * p.Hq + h] = den != 0.f ? top * kLn2 + logf(den) : -INFINITY;
   }
 }
 

@@ -393,6 +393,11 @@ typedef enum {
  *     slopes given: x += slopes[h] * (j - pos)
  * and out = softmax(x) . v over them; query head h reads kv head h / (Hq/Hkv).
  * A row that sees no key (pos < 0) is zero, with lse = -inf.
+ * A NaN in a query, or in a key it sees, makes its row and lse NaN.  A NaN or an
+ * infinity in a value (or an infinite scale) reaches the rows that see it, and on
+ * the tensor-core paths may reach rows of the same sequence that do not see that
+ * token yet but are computed with one that does; rows of the cache that no new
+ * row sees reach nothing.
  *   q, out   : [total_q, Hq, d], any token / head strides, dtype F32 (F32,
  *              E4M3, INT8 caches) or BF16 (BF16, E4M3, INT8 caches).  out
  *              must not overlap q or the cache.

@@ -564,3 +564,51 @@ def test_window_past_32_bits():
     for window in (-1, -2 ** 32 + 1):
         with pytest.raises(S.SdpaError):
             S.sdpa_paged(q, cache, table, lens, window=window)
+
+
+@pytest.mark.parametrize("kw", [{}, dict(window=40), dict(softcap=5.0), dict(slopes=True)], ids=str)
+@pytest.mark.parametrize("path,kv,n", [("exact", [300, 90], [5, 2]), ("exact", [40], [1]), ("decode", [300, 90, 2500], [5, 1, 2]),
+                                       ("tcgen05", [300, 90], [200, 64]), ("tcgen05", [2500], [130])], ids=str)
+@pytest.mark.parametrize("cdt", [BF16, E4M3])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_in_a_key_reaches_the_rows_that_see_it(d, cdt, path, kv, n, kw):
+    """NaN in a key (one, then every one of a sequence) or a query makes NaN of
+    the rows whose scores it is in, their log-sum-exp too, and nothing else."""
+    kw = dict(kw)
+    pool = R.Pool(cdt, 2, d, 16, kv, seed=4)
+    Hq, T = 4, sum(n)
+    q = torch.randn(T, Hq, d, generator=torch.Generator().manual_seed(5)).to(BF16).cuda()
+    if kw.pop("slopes", False):
+        kw["slopes"] = torch.tensor([-0.5, 0.0, 0.25, 0.01], device="cuda")
+    cache, table, lens = pool.cache(), pool.table.cuda(), pool.lens.cuda()
+
+    def run(q):
+        lse = torch.empty(T, Hq, device="cuda")
+        out = S.sdpa_paged(q, cache, table, lens, cu(n), max_q=max(n), lse=lse, path=path, **kw)
+        assert device_error() == 0
+        return out, lse
+
+    clean, clean_lse = run(q)
+    assert torch.isfinite(clean).all() and torch.isfinite(clean_lse).all()
+    b, at = 0, kv[0] - max(2, n[0] // 2)  # between the new rows where there are several
+    pos = torch.arange(n[b]) + kv[b] - n[b]
+    w = kw.get("window") or 1 << 30
+    for keys in ([at], list(range(kv[b]))):
+        kept = cache.k.clone()
+        for j in keys:
+            cache.k[int(pool.table[b, j // 16]), 1, j % 16, 3] = math.nan
+        bad = torch.zeros(T, Hq, dtype=torch.bool)
+        for j in keys:
+            bad[:n[b], 2:] |= ((pos >= j) & (pos - w < j))[:, None]
+        out, lse = run(q)
+        bad = bad.cuda()
+        assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+        assert torch.equal(out[~bad], clean[~bad]) and torch.equal(lse[~bad], clean_lse[~bad])
+        cache.k.copy_(kept)
+    q2 = q.clone()
+    q2[T - 1, 1, 7] = math.nan
+    out, lse = run(q2)
+    bad = torch.zeros(T, Hq, dtype=torch.bool, device="cuda")
+    bad[T - 1, 1] = True
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    assert torch.equal(out[~bad], clean[~bad]) and torch.equal(lse[~bad], clean_lse[~bad])
