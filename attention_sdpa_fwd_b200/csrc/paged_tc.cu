@@ -195,7 +195,7 @@ __device__ __forceinline__ void cap4(uint64_t& x, uint64_t& y, float cap_in, flo
 }
 
 // MOD: 0 plain scores and a positive scale, 1 with slopes (which may be zero), 2
-// capped and with slopes.
+// capped and with slopes, 3 the same for caps above kPlainCap.
 template <int KV, int D, int MOD>
 __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __grid_constant__ TcPagedArgs args) {
   using L = TcLayout<KV, D>;
@@ -663,7 +663,8 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
     auto at_least = [](float x) { return MOD == 0 ? fmaxf(x, 1.5e-36f) : x; };
     const uint64_t xs2 = f2(at_least(xs), at_least(xs));
     const float slope = MOD && p.slopes && row_valid ? __ldg(p.slopes + h) * kLog2e : 0.f;
-    const float cap_in = MOD == 2 ? 2.f / p.softcap : 0.f;  // of scores in log2 units
+    // of scores in log2 units
+    const float cap_in = MOD == 2 ? 2.f / p.softcap : MOD == 3 ? kLn2 / p.softcap : 0.f;
     const float cap_out = p.softcap * kLog2e;
     // groups of keys with an exponent offset of their own: V's scales, the slope's part of a group
     constexpr int NG = kCodes || MOD ? 4 : 1;
@@ -729,6 +730,12 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
               x2[c] = f2_add(x2[c], ramp);
               ramp = f2_add(ramp, two);
             }
+          }
+          if constexpr (MOD == 3) {
+            float v0, v1;
+            f2_split(f2_mul(s2, gx2[y]), v0, v1);
+            x2[c] = f2_add(f2(cap_any(v0, cap_out, cap_in), cap_any(v1, cap_out, cap_in)), ramp);
+            ramp = f2_add(ramp, two);
           }
           if constexpr (MOD == 1) ramp = f2_add(ramp, two);
         }
@@ -955,10 +962,13 @@ bool q_map(CUtensorMap* m, const PagedParams& p, int tok) {
 template <int KV, int D>
 cudaError_t tc_one(const TcPagedArgs& a, int mod, long long units, cudaStream_t stream) {
   using L = TcLayout<KV, D>;
-  auto kern = mod == 0 ? paged_tc_kernel<KV, D, 0> : mod == 1 ? paged_tc_kernel<KV, D, 1> : paged_tc_kernel<KV, D, 2>;
+  auto kern = mod == 0   ? paged_tc_kernel<KV, D, 0>
+              : mod == 1 ? paged_tc_kernel<KV, D, 1>
+              : mod == 2 ? paged_tc_kernel<KV, D, 2>
+                         : paged_tc_kernel<KV, D, 3>;
   static std::mutex mu;
-  static uint64_t done[3];
-  static cudaError_t bad[3];
+  static uint64_t done[4];
+  static cudaError_t bad[4];
   {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1037,7 +1047,7 @@ cudaError_t launch_paged_tc(const PagedParams& p, int limit, void* ws, cudaStrea
     a.ws_o = static_cast<float*>(ws);
     a.ws_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + up256(parts * 256 * c.d * 4));
   }
-  const int mod = p.softcap > 0.f ? 2 : p.slopes != nullptr || !(p.scale > 0.f) ? 1 : 0;
+  const int mod = p.softcap > kPlainCap ? 3 : p.softcap > 0.f ? 2 : p.slopes != nullptr || !(p.scale > 0.f) ? 1 : 0;
   const bool wide = c.d == 128;
   switch (c.dtype) {
     case SDPA_CACHE_BF16: return wide ? tc_one<KV_BF16, 128>(a, mod, units, stream) : tc_one<KV_BF16, 64>(a, mod, units, stream);
