@@ -105,7 +105,9 @@ int build_paged(const void* q, const sdpa_rows_t* qs, const sdpa_cache_t* cache,
   p->q = q; p->out = out; p->lse = lse; p->slopes = slopes;
   p->qt = a.t; p->qh = a.h; p->ot = o.t; p->oh = o.h;
   p->Hq = Hq; p->group = Hq / p->c.Hkv;
-  p->scale = scale; p->softcap = softcap;
+  p->scale = scale;
+  // 1 / c stays finite, so that a score of 0 stays 0; below this a capped score is as good as 0 anyway
+  p->softcap = softcap > 0.f ? fmaxf(softcap, 1e-37f) : 0.f;
   // a window that no sequence of the table can leave is none
   p->window = window >= (long long)p->s.max_pages * p->c.page_size ? 0 : window;
   const int T = p->s.total_q;

@@ -25,7 +25,7 @@ import paged_ref as R
 pytestmark = pytest.mark.gpu
 
 F32, BF16, E4M3, INT8 = torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.int8
-CAPS = [1e-30, 1e-3, 30.0, 128.0, 128.5, 1e3, 1e4, 1e6, 1e30, 3e38]
+CAPS = [1e-40, 1e-30, 1e-3, 30.0, 128.0, 128.5, 1e3, 1e4, 1e6, 1e30, 3e38]
 
 
 def attend(pool, q, n, cap, slopes, u_p, p_floor, u_kv):
