@@ -922,12 +922,13 @@ __global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const __g
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
 // Units a call may have: every sequence with rows for this kernel ends in one
-// unfilled block.
+// unfilled block.  One at least where rows are given, however few max_q allows:
+// the kernel reports the ranges that break it.
 long long unit_bound(const PagedParams& p, int limit) {
   const long long tok2 = 2 * (kRows / p.group);
   const long long least = limit / p.group + 1;  // tokens of a sequence that is not the decode kernel's
   const long long seqs = p.s.total_q / least < p.s.B ? p.s.total_q / least : p.s.B;
-  const long long per = (p.s.max_q + tok2 - 1) / tok2;
+  const long long per = p.s.max_q > 0 ? (p.s.max_q + tok2 - 1) / tok2 : 1;
   const long long a = p.s.total_q / tok2 + seqs, b = seqs * per;
   return (a < b ? a : b) * p.c.Hkv;
 }

@@ -612,3 +612,15 @@ def test_nan_in_a_key_reaches_the_rows_that_see_it(d, cdt, path, kv, n, kw):
     bad[T - 1, 1] = True
     assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
     assert torch.equal(out[~bad], clean[~bad]) and torch.equal(lse[~bad], clean_lse[~bad])
+
+
+@pytest.mark.parametrize("path", ["exact", "decode", "tcgen05", "auto"])
+def test_no_new_rows_announced(path):
+    """max_q 0: sequences that bring rows all the same are reported, rows that
+    belong to nobody are kept."""
+    assert bad_batch(path, max_q=0) == -7
+    pool = R.Pool(BF16, 2, 64, 16, [100, 60], seed=2)
+    out = torch.full((4, 8, 64), 7.0, dtype=BF16, device="cuda")
+    S.sdpa_paged(torch.zeros_like(out), pool.cache(), pool.table.cuda(), pool.lens.cuda(), cu([0, 0]), max_q=0, out=out,
+                 path=path)
+    assert device_error() == 0 and (out == 7).all()
