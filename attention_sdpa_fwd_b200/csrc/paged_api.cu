@@ -36,6 +36,20 @@ long long last3(const sdpa_strides_t& s, long long nb, long long nh, long long n
 long long last2(const sdpa_rows_t& s, long long nt, long long nh, long long d) {
   return nt <= 0 || nh <= 0 ? 0 : (nt - 1) * s.t + (nh - 1) * s.h + d;
 }
+// What a cache occupies: pages, and the scales of codes.
+struct CacheSpans {
+  Span part[4];
+  bool meets(const Span& s) const { return meet(s, part[0]) || meet(s, part[1]) || meet(s, part[2]) || meet(s, part[3]); }
+};
+CacheSpans spans_of(const sdpa_cache_t& c) {
+  auto axis = [&](const void* p, const sdpa_strides_t& st, long long d, size_t esz) {
+    return span_of(p, last3(st, c.num_pages, c.Hkv, c.page_size, d), esz);
+  };
+  const bool codes = is_codes(c.dtype);
+  return {{axis(c.k, c.k_strides, c.d, cache_esz(c.dtype)), axis(c.v, c.v_strides, c.d, cache_esz(c.dtype)),
+           axis(codes ? c.k_scale : nullptr, c.k_scale_strides, 1, 4),
+           axis(codes ? c.v_scale : nullptr, c.v_scale_strides, 1, 4)}};
+}
 
 int check_cache(const sdpa_cache_t* c, CacheView* v) {
   if (c == nullptr) return SDPA_ERR_INVALID_ARG;
@@ -113,15 +127,13 @@ int build_paged(const void* q, const sdpa_rows_t* qs, const sdpa_cache_t* cache,
   const int T = p->s.total_q;
   if (T == 0) return SDPA_OK;
   if (q == nullptr || out == nullptr) return SDPA_ERR_INVALID_ARG;
-  const size_t esz = dtype == SDPA_F32 ? 4 : 2, ce = cache_esz(p->c.dtype);
+  const size_t esz = dtype == SDPA_F32 ? 4 : 2;
   if (!aligned_to(q, esz) || !aligned_to(out, esz) || !aligned_to(lse, 4) || !aligned_to(slopes, 4))
     return SDPA_ERR_MISALIGNED;
   const Span sq = span_of(q, last2(a, T, Hq, d), esz), so = span_of(out, last2(o, T, Hq, d), esz);
   const Span sl = span_of(lse, (long long)T * Hq, 4);
-  const Span sk = span_of(cache->k, last3(cache->k_strides, cache->num_pages, cache->Hkv, cache->page_size, d), ce);
-  const Span sv = span_of(cache->v, last3(cache->v_strides, cache->num_pages, cache->Hkv, cache->page_size, d), ce);
-  if (meet(so, sq) || meet(so, sk) || meet(so, sv) || meet(sl, so) || meet(sl, sq) || meet(sl, sk) || meet(sl, sv))
-    return SDPA_ERR_INVALID_ARG;
+  const CacheSpans pool = spans_of(*cache);
+  if (meet(so, sq) || pool.meets(so) || meet(sl, so) || meet(sl, sq) || pool.meets(sl)) return SDPA_ERR_INVALID_ARG;
   return SDPA_OK;
 }
 
@@ -187,12 +199,11 @@ extern "C" int sdpa_cache_write(const sdpa_cache_t* cache, const sdpa_batch_t* b
   if (s.total_q == 0) return SDPA_OK;
   if ((long long)s.total_q * 2 * c.Hkv > 0x7fffffffLL) return SDPA_ERR_UNSUPPORTED;
   if (k == nullptr || v == nullptr) return SDPA_ERR_INVALID_ARG;
-  const size_t esz = dtype == SDPA_F32 ? 4 : 2, ce = cache_esz(c.dtype);
+  const size_t esz = dtype == SDPA_F32 ? 4 : 2;
   if (!aligned_to(k, esz) || !aligned_to(v, esz)) return SDPA_ERR_MISALIGNED;
   const Span sk = span_of(k, last2(ks, s.total_q, c.Hkv, c.d), esz), sv = span_of(v, last2(vs, s.total_q, c.Hkv, c.d), esz);
-  const Span ck = span_of(c.k, last3(cache->k_strides, c.num_pages, c.Hkv, c.page_size, c.d), ce);
-  const Span cv = span_of(c.v, last3(cache->v_strides, c.num_pages, c.Hkv, c.page_size, c.d), ce);
-  if (meet(sk, ck) || meet(sk, cv) || meet(sv, ck) || meet(sv, cv)) return SDPA_ERR_INVALID_ARG;
+  const CacheSpans pool = spans_of(*cache);
+  if (pool.meets(sk) || pool.meets(sv)) return SDPA_ERR_INVALID_ARG;
   int* err = error_word();
   if (err == nullptr) return SDPA_ERR_CUDA;
   return launch_cache_write(c, s, k, ks.t, ks.h, v, vs.t, vs.h, dtype, err, stream) == cudaSuccess ? SDPA_OK
@@ -217,12 +228,11 @@ extern "C" int sdpa_cache_read(const sdpa_cache_t* cache, const sdpa_batch_t* ba
   if (!stride_ok(ks) || !stride_ok(vs)) return SDPA_ERR_INVALID_ARG;
   if ((long long)s.B * 2 * c.Hkv * ((T + 31) / 32) > 0x7fffffffLL) return SDPA_ERR_UNSUPPORTED;
   if (k_out == nullptr || v_out == nullptr) return SDPA_ERR_INVALID_ARG;
-  const size_t esz = dtype == SDPA_F32 ? 4 : 2, ce = cache_esz(c.dtype);
+  const size_t esz = dtype == SDPA_F32 ? 4 : 2;
   if (!aligned_to(k_out, esz) || !aligned_to(v_out, esz)) return SDPA_ERR_MISALIGNED;
   const Span ok = span_of(k_out, last3(ks, s.B, c.Hkv, T, c.d), esz), ov = span_of(v_out, last3(vs, s.B, c.Hkv, T, c.d), esz);
-  const Span ck = span_of(c.k, last3(cache->k_strides, c.num_pages, c.Hkv, c.page_size, c.d), ce);
-  const Span cv = span_of(c.v, last3(cache->v_strides, c.num_pages, c.Hkv, c.page_size, c.d), ce);
-  if (meet(ok, ck) || meet(ok, cv) || meet(ov, ck) || meet(ov, cv)) return SDPA_ERR_INVALID_ARG;
+  const CacheSpans pool = spans_of(*cache);
+  if (pool.meets(ok) || pool.meets(ov)) return SDPA_ERR_INVALID_ARG;
   int* err = error_word();
   if (err == nullptr) return SDPA_ERR_CUDA;
   return launch_cache_read(c, s, k_out, ks, v_out, vs, dtype, T, err, stream) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;

@@ -323,6 +323,9 @@ int sdpa_fwd_split_kv_static(const void* q, const void* k, const void* v, void* 
  * page 0, a bad row is not written, a bad query range is empty -- and sets the
  * device error word (sdpa_last_device_error: SDPA_ERR_DEVICE_INDEX); the
  * results of that sequence are then unspecified.
+ *
+ * Tensors that must not overlap are compared by their address spans, an E4M3 or
+ * INT8 cache's scales among them (SDPA_ERR_INVALID_ARG).
  */
 typedef enum { SDPA_CACHE_F32 = 0, SDPA_CACHE_BF16 = 1, SDPA_CACHE_E4M3 = 2, SDPA_CACHE_INT8 = 3 } sdpa_cache_dtype_t;
 

@@ -188,3 +188,13 @@ def test_read_refuses_rows_past_the_longest_sequence():
     for T in ((1 << 30) + 1, (1 << 31) - 32, (1 << 31) - 1):
         assert read(cache(Hkv=1), batch(B=1), T=T) == -2
         assert read(cache(Hkv=1), batch(B=1), ks=one, vs=one, T=T) == -2
+
+
+@pytest.mark.parametrize("where", ["ks", "vs", "inside"])
+def test_scales_are_not_overwritten(where):
+    """An 8-bit cache's scales are as much of it as its codes."""
+    c = cache(dtype=E4)
+    at = {"ks": KS, "vs": VS, "inside": KS + 256}[where]
+    assert paged(c, out=at) == -1 and paged(c, lse=at) == -1
+    assert write(c, k=at) == -1 and write(c, v=at) == -1
+    assert read(c, k=at) == -1 and read(c, v=at) == -1
