@@ -22,23 +22,30 @@ bool stride_ok(const sdpa_strides_t& s) {
 }
 bool stride_ok(const sdpa_rows_t& s) { return s.t >= 1 && s.h >= 1 && s.t <= kMaxStride && s.h <= kMaxStride; }
 
+// Addresses [lo, hi) of a tensor; lo > hi: it does not end inside the address space.
 struct Span {
   uintptr_t lo, hi;
+  bool fits() const { return lo <= hi; }
 };
-Span span_of(const void* p, long long elems, size_t esz) {
+// Strides go to 2^40 and extents to 2^31: counted in 128 bits.
+Span span_of(const void* p, __int128 elems, size_t esz) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return {a, p == nullptr || elems <= 0 ? a : a + (size_t)elems * esz};
+  if (p == nullptr || elems <= 0) return {a, a};
+  const __int128 end = (__int128)a + elems * (__int128)esz;
+  return end > (__int128)INT64_MAX ? Span{1, 0} : Span{a, (uintptr_t)end};
 }
 bool meet(const Span& a, const Span& b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-long long last3(const sdpa_strides_t& s, long long nb, long long nh, long long nt, long long d) {
-  return nb <= 0 || nh <= 0 || nt <= 0 ? 0 : (nb - 1) * s.b + (nh - 1) * s.h + (nt - 1) * s.t + d;
+__int128 last3(const sdpa_strides_t& s, long long nb, long long nh, long long nt, long long d) {
+  return nb <= 0 || nh <= 0 || nt <= 0 ? 0 : (__int128)(nb - 1) * s.b + (__int128)(nh - 1) * s.h + (__int128)(nt - 1) * s.t + d;
 }
-long long last2(const sdpa_rows_t& s, long long nt, long long nh, long long d) {
-  return nt <= 0 || nh <= 0 ? 0 : (nt - 1) * s.t + (nh - 1) * s.h + d;
+__int128 last2(const sdpa_rows_t& s, long long nt, long long nh, long long d) {
+  return nt <= 0 || nh <= 0 ? 0 : (__int128)(nt - 1) * s.t + (__int128)(nh - 1) * s.h + d;
 }
+
 // What a cache occupies: pages, and the scales of codes.
 struct CacheSpans {
   Span part[4];
+  bool fits() const { return part[0].fits() && part[1].fits() && part[2].fits() && part[3].fits(); }
   bool meets(const Span& s) const { return meet(s, part[0]) || meet(s, part[1]) || meet(s, part[2]) || meet(s, part[3]); }
 };
 CacheSpans spans_of(const sdpa_cache_t& c) {
@@ -51,7 +58,7 @@ CacheSpans spans_of(const sdpa_cache_t& c) {
            axis(codes ? c.v_scale : nullptr, c.v_scale_strides, 1, 4)}};
 }
 
-int check_cache(const sdpa_cache_t* c, CacheView* v) {
+int check_cache(const sdpa_cache_t* c, CacheView* v, CacheSpans* pool) {
   if (c == nullptr) return SDPA_ERR_INVALID_ARG;
   if (c->dtype < SDPA_CACHE_F32 || c->dtype > SDPA_CACHE_INT8) return SDPA_ERR_INVALID_ARG;
   if (c->num_pages < 1 || c->page_size < 1 || c->Hkv < 1) return SDPA_ERR_INVALID_ARG;
@@ -65,6 +72,8 @@ int check_cache(const sdpa_cache_t* c, CacheView* v) {
   }
   const size_t esz = cache_esz(c->dtype);
   if (!aligned_to(c->k, esz) || !aligned_to(c->v, esz)) return SDPA_ERR_MISALIGNED;
+  *pool = spans_of(*c);
+  if (!pool->fits()) return SDPA_ERR_INVALID_ARG;
   memset(v, 0, sizeof(*v));
   v->k = c->k; v->v = c->v;
   v->kp = c->k_strides.b; v->kh = c->k_strides.h; v->kt = c->k_strides.t;
@@ -105,7 +114,8 @@ int build_paged(const void* q, const sdpa_rows_t* qs, const sdpa_cache_t* cache,
                 const float* slopes, float* lse, PagedParams* p) {
   memset(p, 0, sizeof(*p));
   if (dtype != SDPA_F32 && dtype != SDPA_BF16) return SDPA_ERR_INVALID_ARG;
-  int rc = check_cache(cache, &p->c);
+  CacheSpans pool;
+  int rc = check_cache(cache, &p->c, &pool);
   if (rc == SDPA_OK) rc = check_batch(batch, p->c, true, &p->s);
   if (rc != SDPA_OK) return rc;
   if (Hq < 1 || Hq % p->c.Hkv != 0) return SDPA_ERR_INVALID_ARG;
@@ -132,7 +142,7 @@ int build_paged(const void* q, const sdpa_rows_t* qs, const sdpa_cache_t* cache,
     return SDPA_ERR_MISALIGNED;
   const Span sq = span_of(q, last2(a, T, Hq, d), esz), so = span_of(out, last2(o, T, Hq, d), esz);
   const Span sl = span_of(lse, (long long)T * Hq, 4);
-  const CacheSpans pool = spans_of(*cache);
+  if (!sq.fits() || !so.fits() || !sl.fits()) return SDPA_ERR_INVALID_ARG;
   if (meet(so, sq) || pool.meets(so) || meet(sl, so) || meet(sl, sq) || pool.meets(sl)) return SDPA_ERR_INVALID_ARG;
   return SDPA_OK;
 }
@@ -189,7 +199,8 @@ extern "C" int sdpa_cache_write(const sdpa_cache_t* cache, const sdpa_batch_t* b
   CacheView c;
   BatchView s;
   if (dtype != SDPA_F32 && dtype != SDPA_BF16) return SDPA_ERR_INVALID_ARG;
-  int rc = check_cache(cache, &c);
+  CacheSpans pool;
+  int rc = check_cache(cache, &c, &pool);
   if (rc == SDPA_OK) rc = check_batch(batch, c, true, &s);
   if (rc != SDPA_OK) return rc;
   if (!is_codes(c.dtype) && (c.dtype == SDPA_CACHE_F32) != (dtype == SDPA_F32)) return SDPA_ERR_UNSUPPORTED;
@@ -202,8 +213,7 @@ extern "C" int sdpa_cache_write(const sdpa_cache_t* cache, const sdpa_batch_t* b
   const size_t esz = dtype == SDPA_F32 ? 4 : 2;
   if (!aligned_to(k, esz) || !aligned_to(v, esz)) return SDPA_ERR_MISALIGNED;
   const Span sk = span_of(k, last2(ks, s.total_q, c.Hkv, c.d), esz), sv = span_of(v, last2(vs, s.total_q, c.Hkv, c.d), esz);
-  const CacheSpans pool = spans_of(*cache);
-  if (pool.meets(sk) || pool.meets(sv)) return SDPA_ERR_INVALID_ARG;
+  if (!sk.fits() || !sv.fits() || pool.meets(sk) || pool.meets(sv)) return SDPA_ERR_INVALID_ARG;
   int* err = error_word();
   if (err == nullptr) return SDPA_ERR_CUDA;
   return launch_cache_write(c, s, k, ks.t, ks.h, v, vs.t, vs.h, dtype, err, stream) == cudaSuccess ? SDPA_OK
@@ -217,7 +227,8 @@ extern "C" int sdpa_cache_read(const sdpa_cache_t* cache, const sdpa_batch_t* ba
   BatchView s;
   if (dtype != SDPA_F32 && dtype != SDPA_BF16) return SDPA_ERR_INVALID_ARG;
   if (T < 0) return SDPA_ERR_INVALID_ARG;
-  int rc = check_cache(cache, &c);
+  CacheSpans pool;
+  int rc = check_cache(cache, &c, &pool);
   if (rc == SDPA_OK) rc = check_batch(batch, c, false, &s);
   if (rc != SDPA_OK) return rc;
   if (T > kMaxTokens) return SDPA_ERR_UNSUPPORTED;
@@ -231,8 +242,7 @@ extern "C" int sdpa_cache_read(const sdpa_cache_t* cache, const sdpa_batch_t* ba
   const size_t esz = dtype == SDPA_F32 ? 4 : 2;
   if (!aligned_to(k_out, esz) || !aligned_to(v_out, esz)) return SDPA_ERR_MISALIGNED;
   const Span ok = span_of(k_out, last3(ks, s.B, c.Hkv, T, c.d), esz), ov = span_of(v_out, last3(vs, s.B, c.Hkv, T, c.d), esz);
-  const CacheSpans pool = spans_of(*cache);
-  if (pool.meets(ok) || pool.meets(ov)) return SDPA_ERR_INVALID_ARG;
+  if (!ok.fits() || !ov.fits() || pool.meets(ok) || pool.meets(ov)) return SDPA_ERR_INVALID_ARG;
   int* err = error_word();
   if (err == nullptr) return SDPA_ERR_CUDA;
   return launch_cache_read(c, s, k_out, ks, v_out, vs, dtype, T, err, stream) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;

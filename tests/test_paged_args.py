@@ -198,3 +198,22 @@ def test_scales_are_not_overwritten(where):
     assert paged(c, out=at) == -1 and paged(c, lse=at) == -1
     assert write(c, k=at) == -1 and write(c, v=at) == -1
     assert read(c, k=at) == -1 and read(c, v=at) == -1
+
+
+@pytest.mark.parametrize("which", ["k_strides", "v_strides", "k_scale_strides", "v_scale_strides"])
+def test_pools_past_the_address_space(which):
+    """(num_pages - 1) times the page stride is 2^64: as 64 bits it would be 0
+    and an overlap behind the first page unseen."""
+    st = dict.fromkeys(("k_strides", "v_strides", "k_scale_strides", "v_scale_strides"), S.sdpa_strides_t(1, 1024, 64))
+    st[which] = S.sdpa_strides_t(1 << 40, 1024, 64)
+    c = cache(dtype=E4, num_pages=(1 << 24) + 1, **st)
+    for call in (paged, write, read):
+        assert call(c) == -1
+
+
+def test_rows_past_the_address_space():
+    far, b = S.sdpa_rows_t(1 << 40, 64), batch(total_q=(1 << 24) + 1)
+    assert paged(None, b, qs=far) == -1 and paged(None, b, os=far) == -1
+    assert write(None, b, ks=far) == -1 and write(None, b, vs=far) == -1
+    far, b = S.sdpa_strides_t(1 << 40, 640, 64), batch(B=(1 << 24) + 1)
+    assert read(None, b, ks=far) == -1 and read(None, b, vs=far) == -1
