@@ -5,6 +5,9 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
+#include <initializer_list>
+
 #include "paged.cuh"
 
 namespace sdpa {
@@ -57,6 +60,13 @@ CacheSpans spans_of(const sdpa_cache_t& c) {
            axis(codes ? c.k_scale : nullptr, c.k_scale_strides, 1, 4),
            axis(codes ? c.v_scale : nullptr, c.v_scale_strides, 1, 4)}};
 }
+// What the kernels read of a batch.
+struct BatchSpans {
+  Span part[3];
+  bool fits() const { return part[0].fits() && part[1].fits() && part[2].fits(); }
+  bool meets(const Span& s) const { return meet(s, part[0]) || meet(s, part[1]) || meet(s, part[2]); }
+  bool meets(const CacheSpans& c) const { return c.meets(part[0]) || c.meets(part[1]) || c.meets(part[2]); }
+};
 
 int check_cache(const sdpa_cache_t* c, CacheView* v, CacheSpans* pool) {
   if (c == nullptr) return SDPA_ERR_INVALID_ARG;
@@ -88,13 +98,16 @@ int check_cache(const sdpa_cache_t* c, CacheView* v, CacheSpans* pool) {
   return SDPA_OK;
 }
 
-int check_batch(const sdpa_batch_t* s, const CacheView& c, bool rows, BatchView* v) {
+int check_batch(const sdpa_batch_t* s, const CacheView& c, bool rows, BatchView* v, BatchSpans* read) {
   if (s == nullptr) return SDPA_ERR_INVALID_ARG;
   if (s->B < 0 || s->max_pages < 0 || s->table_stride < s->max_pages) return SDPA_ERR_INVALID_ARG;
   if ((long long)s->max_pages * c.page_size > kMaxTokens) return SDPA_ERR_UNSUPPORTED;
   if (s->B > 0 && s->kv_lens == nullptr) return SDPA_ERR_INVALID_ARG;
   if (s->B > 0 && s->max_pages > 0 && s->page_table == nullptr) return SDPA_ERR_INVALID_ARG;
   if (!aligned_to(s->page_table, 4) || !aligned_to(s->kv_lens, 4) || !aligned_to(s->cu_q, 4)) return SDPA_ERR_MISALIGNED;
+  *read = {{span_of(s->max_pages > 0 ? s->page_table : nullptr, (__int128)(s->B - 1) * s->table_stride + s->max_pages, 4),
+            span_of(s->kv_lens, s->B, 4), span_of(rows ? s->cu_q : nullptr, s->B + 1LL, 4)}};
+  if (!read->fits()) return SDPA_ERR_INVALID_ARG;
   memset(v, 0, sizeof(*v));
   v->table = s->page_table; v->table_stride = s->table_stride; v->max_pages = s->max_pages;
   v->kv_lens = s->kv_lens; v->B = s->B;
@@ -115,8 +128,9 @@ int build_paged(const void* q, const sdpa_rows_t* qs, const sdpa_cache_t* cache,
   memset(p, 0, sizeof(*p));
   if (dtype != SDPA_F32 && dtype != SDPA_BF16) return SDPA_ERR_INVALID_ARG;
   CacheSpans pool;
+  BatchSpans read;
   int rc = check_cache(cache, &p->c, &pool);
-  if (rc == SDPA_OK) rc = check_batch(batch, p->c, true, &p->s);
+  if (rc == SDPA_OK) rc = check_batch(batch, p->c, true, &p->s, &read);
   if (rc != SDPA_OK) return rc;
   if (Hq < 1 || Hq % p->c.Hkv != 0) return SDPA_ERR_INVALID_ARG;
   if (Hq > 65535) return SDPA_ERR_UNSUPPORTED;
@@ -142,8 +156,10 @@ int build_paged(const void* q, const sdpa_rows_t* qs, const sdpa_cache_t* cache,
     return SDPA_ERR_MISALIGNED;
   const Span sq = span_of(q, last2(a, T, Hq, d), esz), so = span_of(out, last2(o, T, Hq, d), esz);
   const Span sl = span_of(lse, (long long)T * Hq, 4);
-  if (!sq.fits() || !so.fits() || !sl.fits()) return SDPA_ERR_INVALID_ARG;
-  if (meet(so, sq) || pool.meets(so) || meet(sl, so) || meet(sl, sq) || pool.meets(sl)) return SDPA_ERR_INVALID_ARG;
+  const Span ss = span_of(slopes, Hq, 4);
+  if (!sq.fits() || !so.fits() || !sl.fits() || meet(so, sl)) return SDPA_ERR_INVALID_ARG;
+  for (const Span& s : {so, sl})
+    if (meet(s, sq) || meet(s, ss) || pool.meets(s) || read.meets(s)) return SDPA_ERR_INVALID_ARG;
   return SDPA_OK;
 }
 
@@ -200,8 +216,9 @@ extern "C" int sdpa_cache_write(const sdpa_cache_t* cache, const sdpa_batch_t* b
   BatchView s;
   if (dtype != SDPA_F32 && dtype != SDPA_BF16) return SDPA_ERR_INVALID_ARG;
   CacheSpans pool;
+  BatchSpans read;
   int rc = check_cache(cache, &c, &pool);
-  if (rc == SDPA_OK) rc = check_batch(batch, c, true, &s);
+  if (rc == SDPA_OK) rc = check_batch(batch, c, true, &s, &read);
   if (rc != SDPA_OK) return rc;
   if (!is_codes(c.dtype) && (c.dtype == SDPA_CACHE_F32) != (dtype == SDPA_F32)) return SDPA_ERR_UNSUPPORTED;
   const sdpa_rows_t dense = {(int64_t)c.Hkv * c.d, c.d};
@@ -213,7 +230,7 @@ extern "C" int sdpa_cache_write(const sdpa_cache_t* cache, const sdpa_batch_t* b
   const size_t esz = dtype == SDPA_F32 ? 4 : 2;
   if (!aligned_to(k, esz) || !aligned_to(v, esz)) return SDPA_ERR_MISALIGNED;
   const Span sk = span_of(k, last2(ks, s.total_q, c.Hkv, c.d), esz), sv = span_of(v, last2(vs, s.total_q, c.Hkv, c.d), esz);
-  if (!sk.fits() || !sv.fits() || pool.meets(sk) || pool.meets(sv)) return SDPA_ERR_INVALID_ARG;
+  if (!sk.fits() || !sv.fits() || pool.meets(sk) || pool.meets(sv) || read.meets(pool)) return SDPA_ERR_INVALID_ARG;
   int* err = error_word();
   if (err == nullptr) return SDPA_ERR_CUDA;
   return launch_cache_write(c, s, k, ks.t, ks.h, v, vs.t, vs.h, dtype, err, stream) == cudaSuccess ? SDPA_OK
@@ -228,8 +245,9 @@ extern "C" int sdpa_cache_read(const sdpa_cache_t* cache, const sdpa_batch_t* ba
   if (dtype != SDPA_F32 && dtype != SDPA_BF16) return SDPA_ERR_INVALID_ARG;
   if (T < 0) return SDPA_ERR_INVALID_ARG;
   CacheSpans pool;
+  BatchSpans read;
   int rc = check_cache(cache, &c, &pool);
-  if (rc == SDPA_OK) rc = check_batch(batch, c, false, &s);
+  if (rc == SDPA_OK) rc = check_batch(batch, c, false, &s, &read);
   if (rc != SDPA_OK) return rc;
   if (T > kMaxTokens) return SDPA_ERR_UNSUPPORTED;
   if (!is_codes(c.dtype) && (c.dtype == SDPA_CACHE_F32) != (dtype == SDPA_F32)) return SDPA_ERR_UNSUPPORTED;
@@ -242,7 +260,11 @@ extern "C" int sdpa_cache_read(const sdpa_cache_t* cache, const sdpa_batch_t* ba
   const size_t esz = dtype == SDPA_F32 ? 4 : 2;
   if (!aligned_to(k_out, esz) || !aligned_to(v_out, esz)) return SDPA_ERR_MISALIGNED;
   const Span ok = span_of(k_out, last3(ks, s.B, c.Hkv, T, c.d), esz), ov = span_of(v_out, last3(vs, s.B, c.Hkv, T, c.d), esz);
-  if (!ok.fits() || !ov.fits() || pool.meets(ok) || pool.meets(ov)) return SDPA_ERR_INVALID_ARG;
+  if (!ok.fits() || !ov.fits()) return SDPA_ERR_INVALID_ARG;
+  for (const Span& s : {ok, ov})
+    if (pool.meets(s) || read.meets(s)) return SDPA_ERR_INVALID_ARG;
+  // the outputs may interleave, as views of one tensor; rows that begin less than a row apart are not two
+  if (std::max(ok.lo, ov.lo) - std::min(ok.lo, ov.lo) < c.d * esz) return SDPA_ERR_INVALID_ARG;
   int* err = error_word();
   if (err == nullptr) return SDPA_ERR_CUDA;
   return launch_cache_read(c, s, k_out, ks, v_out, vs, dtype, T, err, stream) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;

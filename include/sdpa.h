@@ -324,8 +324,9 @@ int sdpa_fwd_split_kv_static(const void* q, const void* k, const void* v, void* 
  * device error word (sdpa_last_device_error: SDPA_ERR_DEVICE_INDEX); the
  * results of that sequence are then unspecified.
  *
- * Tensors that must not overlap are compared by their address spans, an E4M3 or
- * INT8 cache's scales among them (SDPA_ERR_INVALID_ARG).
+ * Nothing a call writes may overlap what it reads: tensors are compared by their
+ * address spans, an E4M3 or INT8 cache's scales, the table, lengths and cu_q
+ * among them (SDPA_ERR_INVALID_ARG).
  */
 typedef enum { SDPA_CACHE_F32 = 0, SDPA_CACHE_BF16 = 1, SDPA_CACHE_E4M3 = 2, SDPA_CACHE_INT8 = 3 } sdpa_cache_dtype_t;
 
@@ -370,7 +371,8 @@ int sdpa_cache_write(const sdpa_cache_t* cache, const sdpa_batch_t* batch, const
  * sdpa_cache_read -- the other way: tokens 0 .. min(kv_lens[b], T) - 1 of every
  * sequence into dense k_out, v_out [B, Hkv, T, d] (any strides; NULL: dense
  * bhsd, as sdpa_fwd takes them), dequantised and rounded once to dtype.  Rows
- * past a sequence's tokens are left as they are.
+ * past a sequence's tokens are left as they are.  k_out and v_out may be views
+ * of one tensor but share no element.
  */
 int sdpa_cache_read(const sdpa_cache_t* cache, const sdpa_batch_t* batch, void* k_out, const sdpa_strides_t* k_strides,
                     void* v_out, const sdpa_strides_t* v_strides, sdpa_dtype_t dtype, int T, cudaStream_t stream);

@@ -217,3 +217,17 @@ def test_rows_past_the_address_space():
     assert write(None, b, ks=far) == -1 and write(None, b, vs=far) == -1
     far, b = S.sdpa_strides_t(1 << 40, 640, 64), batch(B=(1 << 24) + 1)
     assert read(None, b, ks=far) == -1 and read(None, b, vs=far) == -1
+
+
+def test_outputs_are_not_the_batch():
+    """What the kernels read of a batch, and the slopes, are not written over."""
+    for at in (TAB, LEN, LEN + 4, CU, CU + 8):
+        assert paged(None, None, out=at) == -1 and paged(None, None, lse=at) == -1
+        assert write(cache(k=at)) == -1 and write(cache(dtype=E4, v_scale=at)) == -1
+    for at in (TAB, LEN + 4):
+        assert read(k=at) == -1 and read(v=at) == -1
+    assert paged(None, None, slopes=W, out=W) == -1 and paged(None, None, slopes=W + 12, lse=W) == -1
+
+
+def test_read_outputs_are_two():
+    assert read(k=Q, v=Q) == -1 and read(k=Q, v=Q + 126) == -1 and read(k=Q + 64, v=Q) == -1
