@@ -141,7 +141,7 @@ class KVCache:
             c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
             c.k_scale_strides, c.v_scale_strides = _strides(k_scale), _strides(v_scale)
         self._descriptor = c
-        self._workspace = 0  # bytes the last sdpa_paged needed: where the next one starts from
+        self._scratch = (None, 0)  # sizes of the last sdpa_paged and the bytes of scratch it asked for
 
     k = property(lambda self: self._k)
     v = property(lambda self: self._v)
@@ -307,8 +307,9 @@ def sdpa_paged(q, cache: KVCache, page_table, kv_lens, cu_q=None, scale: Optiona
         raise ValueError("lse must be a contiguous float32 [tokens, Hq] tensor on the cache's device")
     desc, code, way = cache.descriptor(), S._dtype_code(q), PAGED_PATHS[path]
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    # to the C int's range (ctypes would keep the low bits only); one past every cache is none there too
-    window = min(max(int(window), -1), 0x7fffffff)
+    if window != 0:  # to the C int's range (ctypes would keep the low bits only); one past every cache is none there too
+        window = min(max(int(window), -1), 0x7fffffff)
+    sizes = (batch.B, T, batch.max_q, batch.max_pages, Hq, window, way)  # what scratch goes by, beside layouts
 
     def call(st):
         nonlocal out
@@ -320,18 +321,21 @@ def sdpa_paged(q, cache: KVCache, page_table, kv_lens, cu_q=None, scale: Optiona
                 raise ValueError("out must have q's shape and dtype")
             os_ = _rows(out, Hq, cache, "out")
         qp, op = q.data_ptr(), out.data_ptr()
+        last, have = cache._scratch
+        if last != sizes:
+            have = 0
         while True:
-            have = cache._workspace
             ws = torch.empty(have, dtype=torch.uint8, device=dev) if have else None
             rc = sdpa_fwd_paged(qp, qs, desc, batch, op, os_, code, Hq, scale, window, float(softcap),
                                 None if slopes is None else slopes.data_ptr(), None if lse is None else lse.data_ptr(),
                                 way, None if ws is None else ws.data_ptr(), have, st)
             if rc != -6:
+                cache._scratch = (sizes, have)
                 return rc
-            # more scratch than the last call on this cache took
+            ws = None
             need = sdpa_fwd_paged_workspace(desc, batch, qp, qs, op, os_, code, Hq, window, way)
             if need <= have:
                 return int(min(need, -6))
-            cache._workspace = need
+            have = need
     _check(_on(dev, stream, call), "sdpa_fwd_paged")
     return out

@@ -624,3 +624,30 @@ def test_no_new_rows_announced(path):
     S.sdpa_paged(torch.zeros_like(out), pool.cache(), pool.table.cuda(), pool.lens.cuda(), cu([0, 0]), max_q=0, out=out,
                  path=path)
     assert device_error() == 0 and (out == 7).all()
+
+
+def test_scratch_goes_by_the_call():
+    """What a call allocates is what sdpa_fwd_paged_workspace asks for it,
+    whatever ran on the cache before."""
+    pool, q, _, _, table, lens = decode_setup(BF16, 64, (4000, 900, 64))
+    cache, short, few = pool.cache(), table[:, :8].contiguous(), lens.clamp(max=100)
+    chunk = torch.randn(200, 8, 64, device="cuda").to(BF16)
+
+    def taken(q, table, lens, n, most):
+        out = torch.empty_like(q)
+        cuq = None if n is None else cu(n)
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        S.sdpa_paged(q, cache, table, lens, cuq, max_q=most, out=out)
+        got = torch.cuda.max_memory_allocated() - before
+        b = S.paged._batch(cache, table, lens, cuq, q.shape[0], most)
+        need = S.sdpa_fwd_paged_workspace(cache.descriptor(), b, q.data_ptr(), None, out.data_ptr(), None, S.SDPA_BF16, 8, 0, 0)
+        assert device_error() == 0 and need <= got <= need + 511, (got, need)  # the allocator's granule
+        return need
+
+    calls = [(q, short, few, None, 1), (q, table, lens, None, 1), (chunk, table, lens, [100, 50, 50], 100)]
+    first = [taken(*c) for c in calls]
+    assert first[0] == 0 < first[1] < first[2]
+    for i in (0, 1, 0, 2, 2, 0):
+        assert taken(*calls[i]) == first[i]
