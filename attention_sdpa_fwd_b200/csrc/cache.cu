@@ -31,7 +31,7 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int t, int lane) {
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int i = lane * step;
-    const unsigned le = __ballot_sync(0xffffffffu, i < n && __ldg(cu + lo + i) <= t);
+    const unsigned le = __ballot_sync(0xffffffffu, i < n && ld_prior(cu + lo + i) <= t);
     const int k = max(0, __popc(le) - 1);
     lo += k * step;
     n = min(step, n - k * step);
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 5) cache_write_kernel(const __grid_c
         if (mine && t < ntok) {
           const T* at = src + t * st;
           if (a.vec) {
-            const uint4 raw = __ldg(reinterpret_cast<const uint4*>(at));
+            const uint4 raw = ld_prior(reinterpret_cast<const uint4*>(at));
             x[u][0] = raw.x; x[u][1] = raw.y; x[u][2] = raw.z; x[u][3] = raw.w;
           } else {
             alignas(16) T e[E];
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 5) cache_write_kernel(const __grid_c
             const int t = t0 + lane;
             int b = t, page = -1, off = 0;
             if (a.s.cu_q)
-              for (b = first; b + 1 < a.s.B && __ldg(a.s.cu_q + b + 1) <= t;) ++b;
+              for (b = first; b + 1 < a.s.B && ld_prior(a.s.cu_q + b + 1) <= t;) ++b;
             const Seq q = seq_of(a.s, a.c, b, a.err);
             // rows behind the last sequence and rows without a place are left out
             if (t >= q.q0 && t < q.q0 + q.n) {
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
       const C* row = src + page[u] * sp + off * stk;
       if (a.vec) {
         using V = Bytes<E * sizeof(C)>;
-        if constexpr (E * sizeof(C) == 16) *reinterpret_cast<uint4*>(raw[u]) = __ldg(reinterpret_cast<const uint4*>(row));
+        if constexpr (E * sizeof(C) == 16) *reinterpret_cast<uint4*>(raw[u]) = ld_prior(reinterpret_cast<const uint4*>(row));
         else *reinterpret_cast<V*>(raw[u]) = *reinterpret_cast<const V*>(row);
       } else {
 #pragma unroll

@@ -58,12 +58,19 @@ struct Seq {
   int q0, n, L;
 };
 
+// A load of what an earlier grid of the stream may have written: the rows and
+// scales another call leaves, lengths, tables.  That grid may still run when this
+// one starts (griddepcontrol), so the read-only path, __ldg, whose data must not
+// change while the grid lives, is not for it.
+template <typename T>
+__device__ __forceinline__ T ld_prior(const T* p) { return *p; }
+
 __device__ __forceinline__ void index_error(int* err) {
   if (err != nullptr) atomicOr(err, ERR_INDEX);
 }
 
 __device__ __forceinline__ int seq_len(const BatchView& s, const CacheView& c, int b, int* err) {
-  const int L = __ldg(s.kv_lens + b);
+  const int L = ld_prior(s.kv_lens + b);
   const long long cap = (long long)s.max_pages * c.page_size;
   if (L < 0 || L > cap) {
     index_error(err);
@@ -78,7 +85,7 @@ __device__ __forceinline__ Seq seq_of(const BatchView& s, const CacheView& c, in
     r.q0 = b;
     r.n = 1;
   } else {
-    const int a = __ldg(s.cu_q + b), e = __ldg(s.cu_q + b + 1);
+    const int a = ld_prior(s.cu_q + b), e = ld_prior(s.cu_q + b + 1);
     const bool ok = a >= 0 && e >= a && e <= s.total_q && e - a <= s.max_q;
     r.q0 = ok ? a : 0;
     r.n = ok ? e - a : 0;
@@ -91,7 +98,7 @@ __device__ __forceinline__ Seq seq_of(const BatchView& s, const CacheView& c, in
 // Page of token t of sequence b as the table has it; a bad one becomes -1 in
 // good_page.  (Apart, so that a load may be on its way long before its use.)
 __device__ __forceinline__ int page_entry(const BatchView& s, const CacheView& c, int b, int t) {
-  return __ldg(s.table + (long long)b * s.table_stride + fdiv((uint32_t)t, c.fd_page));
+  return ld_prior(s.table + (long long)b * s.table_stride + fdiv((uint32_t)t, c.fd_page));
 }
 __device__ __forceinline__ int good_page(const CacheView& c, int p, int* err) {
   if ((unsigned)p < (unsigned)c.num_pages) return p;

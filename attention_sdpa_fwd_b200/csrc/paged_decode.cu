@@ -323,13 +323,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, NT>::kCtas)) paged_decod
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
           uint4 x = make_uint4(0, 0, 0, 0);
-          if (r < u.rows) x = __ldg(reinterpret_cast<const uint4*>(src + c * (D / 4) + k * 8));
+          if (r < u.rows) x = ld_prior(reinterpret_cast<const uint4*>(src + c * (D / 4) + k * 8));
           qw[t][4 * k] = x.x; qw[t][4 * k + 1] = x.y; qw[t][4 * k + 2] = x.z; qw[t][4 * k + 3] = x.w;
         }
       } else {
 #pragma unroll
         for (int k = 0; k < D / 8; ++k)
-          qw[t][k] = r < u.rows ? __ldg(reinterpret_cast<const unsigned int*>(src + 16 * (k >> 1) + 8 * (k & 1) + 2 * c)) : 0u;
+          qw[t][k] = r < u.rows ? ld_prior(reinterpret_cast<const unsigned int*>(src + 16 * (k >> 1) + 8 * (k & 1) + 2 * c)) : 0u;
       }
     }
     pages = max(0, good_page(p.c, pages, p.err));
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KV, D, NT>::kCtas)) paged_decod
         const int r = t * 8 + 2 * c + e;
         const int i = r / p.group, g = r - i * p.group;
         pos[t][e] = u.s.L - u.s.n + i;
-        if constexpr (MOD) slope[t][e] = p.slopes && r < u.rows ? __ldg(p.slopes + hk * p.group + g) : 0.f;
+        if constexpr (MOD) slope[t][e] = p.slopes && r < u.rows ? ld_prior(p.slopes + hk * p.group + g) : 0.f;
         xscale[t][e] = p.scale * (F16 ? s_x[warp * C::kRows + r] : 1.f);
         if constexpr (!MOD) xscale[t][e] *= kLog2e;
       }

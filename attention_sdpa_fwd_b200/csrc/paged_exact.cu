@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_exact_kernel(const __grid_c
       int lo = 0, hi = p.s.B;  // largest b with cu[b] <= t
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (__ldg(p.s.cu_q + mid) <= t) lo = mid; else hi = mid;
+        if (ld_prior(p.s.cu_q + mid) <= t) lo = mid; else hi = mid;
       }
       s_b = lo;
     }
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_exact_kernel(const __grid_c
   for (int i = 0; i < E; ++i) qv[i] = to_f32(qrow[i]);
   const C* kb = static_cast<const C*>(p.c.k) + hk * p.c.kh + e0;
   const C* vb = static_cast<const C*>(p.c.v) + hk * p.c.vh + e0;
-  const float slope = p.slopes ? __ldg(p.slopes + h) : 0.f;
+  const float slope = p.slopes ? ld_prior(p.slopes + h) : 0.f;
 
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll

@@ -496,8 +496,8 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
         if (key >= 0) {
           const long long pg = max(0, good_page(p.c, pg_n, p.err));
           const int off = key - (int)fdiv((uint32_t)key, p.c.fd_page) * p.c.page_size;
-          ks_n = __ldg(p.c.ks + pg * p.c.ksp + u.hk * p.c.ksh + off * p.c.kst);
-          vs_n = __ldg(p.c.vs + pg * p.c.vsp + u.hk * p.c.vsh + off * p.c.vst);
+          ks_n = ld_prior(p.c.ks + pg * p.c.ksp + u.hk * p.c.ksh + off * p.c.kst);
+          vs_n = ld_prior(p.c.vs + pg * p.c.vsp + u.hk * p.c.vsh + off * p.c.vst);
         }
       };
       // The largest scale's exponent less 6, and scale 2^-e of a key as the sum
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
     // become 0 (below 2^-119 every score is as good as 0 anyway)
     auto at_least = [](float x) { return MOD == 0 ? fmaxf(x, 1.5e-36f) : x; };
     const uint64_t xs2 = f2(at_least(xs), at_least(xs));
-    const float slope = MOD && p.slopes && row_valid ? __ldg(p.slopes + h) * kLog2e : 0.f;
+    const float slope = MOD && p.slopes && row_valid ? ld_prior(p.slopes + h) * kLog2e : 0.f;
     // of scores in log2 units
     const float cap_in = MOD == 2 ? 2.f / p.softcap : MOD == 3 ? kLn2 / p.softcap : 0.f;
     const float cap_out = p.softcap * kLog2e;

@@ -651,3 +651,54 @@ def test_scratch_goes_by_the_call():
     assert first[0] == 0 < first[1] < first[2]
     for i in (0, 1, 0, 2, 2, 0):
         assert taken(*calls[i]) == first[i]
+
+
+@pytest.mark.parametrize("cdt,io", [(BF16, BF16), (E4M3, BF16), (INT8, F32)])
+def test_back_to_back_calls_read_what_the_last_one_wrote(cdt, io):
+    """Calls that feed one another with nothing between them: a step's rows are
+    another call's output, its cache is written, attended by single tokens and
+    by a chunk, read back, and the rows read are written again."""
+    n = [400, 30, 260]
+    caches = [S.KVCache.empty(80, 16, 2, 64, cdt) for _ in range(2)]
+    table = torch.randperm(80, generator=torch.Generator().manual_seed(1)).int().cuda()[:78].view(3, 26)
+    lens = torch.tensor(n, dtype=torch.int32, device="cuda")
+    rows = torch.randn(2, sum(n), 2, 64, device="cuda").to(io)
+
+    def steps(wait):
+        outs = []
+        for t in (x for c in caches for x in (c.k, c.v, c.k_scale, c.v_scale) if x is not None):
+            t.zero_()
+        k, v = rows[0].clone(), rows[1].clone()
+        torch.cuda.synchronize()
+        for i in range(6):
+            a, b = caches[i % 2], caches[1 - i % 2]
+            S.cache_write(a, k, v, table, lens, cu_n, max_q=400)
+            wait()
+            one = S.sdpa_paged(q1, a, table, lens)
+            wait()
+            S.sdpa_paged(one, a, table, lens, out=q1b)
+            wait()
+            many = S.sdpa_paged(qn, a, table, lens, cu_n, max_q=400)
+            wait()
+            kd, vd = S.cache_read(a, table, lens, k_out, v_out)
+            wait()
+            # 64 tokens of sequence 0, straight from what was read, into the other cache
+            S.cache_write(b, kd[0].transpose(0, 1)[:64], vd[0].transpose(0, 1)[:64], table[:1], l64, cu64, max_q=64)
+            wait()
+            # and over rows this cache holds: the chunk call behind it sees the new ones
+            S.cache_write(a, many[:64, :2], many[64:128, 2:4], table[:1], l64, cu64, max_q=64)
+            wait()
+            last = S.sdpa_paged(qn[:64], a, table[:1], l64, cu64, max_q=64)
+            wait()
+            outs += [one.clone(), q1b.clone(), many, kd.clone(), vd.clone(), last]
+        return outs
+
+    cu_n, cu64, l64 = cu(n), cu([64]), torch.tensor([64], dtype=torch.int32, device="cuda")
+    q1, q1b = torch.randn(3, 4, 64, device="cuda").to(io), torch.empty(3, 4, 64, device="cuda", dtype=io)
+    qn = torch.randn(sum(n), 4, 64, device="cuda").to(io)
+    k_out, v_out = (torch.zeros(3, 2, 400, 64, device="cuda", dtype=io) for _ in range(2))
+    want = steps(torch.cuda.synchronize)
+    for _ in range(5):
+        for a, b in zip(want, steps(lambda: None)):
+            assert torch.equal(a, b)
+    assert device_error() == 0
