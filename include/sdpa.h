@@ -416,8 +416,8 @@ typedef enum {
  *              16-byte aligned, the call's own until its work on `stream` has
  *              run (SDPA_ERR_CAPACITY when NULL or too small).  Nothing is kept in it
  *              from call to call and it needs no clearing.
- * Values in rows of the cache that the batch's tokens do not cover may be
- * anything; those of V rows it does cover must be finite, seen or not.
+ * Rows of the cache that the batch's tokens do not cover may hold anything, and
+ * so may those in front of every new row's window.
  */
 int sdpa_fwd_paged(const void* q, const sdpa_rows_t* q_strides, const sdpa_cache_t* cache, const sdpa_batch_t* batch,
                void* out, const sdpa_rows_t* out_strides, sdpa_dtype_t dtype, int Hq, float scale, int window,

@@ -94,3 +94,15 @@ def test_parity_through_debug_build(debug_lib):
         "                      'tests/test_parity.py', 'tests/test_random_sweep.py', 'tests/test_strided.py']))\n")
     r = _child(code, timeout=1800)
     assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]
+
+
+@pytest.mark.gpu
+def test_paged_operators_through_debug_build(debug_lib):
+    """A share of the paged operators' tests, every kernel among them, with SDPA_DEBUG=1."""
+    code = (
+        "import sys, pytest, attention_sdpa_fwd_b200 as S\n"
+        "assert S.LIB_PATH == S.DEBUG_LIB_PATH and S.sdpa_debug_checks() == 1\n"
+        "sys.exit(pytest.main(['-q', '-x', '-m', 'gpu', '-p', 'no:cacheprovider', 'tests/test_paged.py', '-k',\n"
+        "                      'write_then_read or exact_every_type or decode_rows or chunk_options or auto_mixed or bad']))\n")
+    r = _child(code, timeout=900)
+    assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]

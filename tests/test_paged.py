@@ -702,3 +702,55 @@ def test_back_to_back_calls_read_what_the_last_one_wrote(cdt, io):
         for a, b in zip(want, steps(lambda: None)):
             assert torch.equal(a, b)
     assert device_error() == 0
+
+
+@pytest.mark.parametrize("path,kv,n", [("exact", [300, 90], [5, 2]), ("decode", [300, 90, 2500], [5, 1, 2]),
+                                       ("tcgen05", [300, 90], [200, 64]), ("tcgen05", [2500], [130])], ids=str)
+@pytest.mark.parametrize("cdt", [BF16, E4M3, INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_that_are_not_finite(d, cdt, path, kv, n):
+    """A NaN or an infinity in a value (INT8: an infinite scale) makes every row
+    that sees it not finite, and touches no other sequence or kv head; in front
+    of every row's window, or behind the sequence's tokens, it touches nothing."""
+    pool = R.Pool(cdt, 2, d, 16, kv, seed=4)
+    T = sum(n)
+    q = torch.randn(T, 4, d, generator=torch.Generator().manual_seed(5)).to(BF16).cuda()
+    cache, table, lens = pool.cache(), pool.table.cuda(), pool.lens.cuda()
+
+    def run(window=0):
+        lse = torch.empty(T, 4, device="cuda")
+        out = S.sdpa_paged(q, cache, table, lens, cu(n), max_q=max(n), window=window, lse=lse, path=path)
+        assert device_error() == 0
+        return out, lse
+
+    def spoil(j, x):
+        p, o = int(pool.table[0, j // 16]), j % 16
+        if cdt == INT8:
+            cache.v_scale[p, 1, o] = math.inf
+        else:
+            row = cache.v[p, 1, o].float()
+            row[3] = x
+            cache.v[p, 1, o] = row.to(cdt)
+
+    first = kv[0] - n[0]
+    clean, clean_lse = run()
+    for j, x in ((0, math.nan), (first, math.nan), (first + 1, math.inf), (kv[0] - 1, math.inf)):
+        if cdt == E4M3 and x == math.inf:
+            x = math.nan  # the type has no infinity
+        kept = [t.clone() for t in (cache.v, cache.v_scale) if t is not None]
+        spoil(j, x)
+        out, lse = run()
+        see = torch.arange(n[0]) + first >= j
+        assert not torch.isfinite(out[:n[0]][see.cuda(), 2:, 3]).any()
+        assert torch.equal(out[:, :2], clean[:, :2]) and torch.equal(out[n[0]:], clean[n[0]:])
+        if cdt != INT8:  # an infinite scale is in the weights' sum too
+            assert torch.equal(lse, clean_lse)
+        for t, old in zip((cache.v, cache.v_scale), kept):
+            t.copy_(old)
+    # in front of the window of the first new row, in its tile and far from it
+    window = 20
+    clean, clean_lse = run(window)
+    for j in (0, first - window, max(0, first - window - 15)):
+        spoil(j, math.nan)
+    out, lse = run(window)
+    assert torch.isfinite(out).all() and torch.equal(out, clean) and torch.equal(lse, clean_lse)
