@@ -500,10 +500,11 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, 1) paged_tc_kernel(const __gri
           vs_n = ld_prior(p.c.vs + pg * p.c.vsp + u.hk * p.c.vsh + off * p.c.vst);
         }
       };
-      // The largest scale's exponent less 6, and scale 2^-e of a key as the sum
-      // of two f16 (the first in the low half).
+      // The largest finite scale's exponent less 6 (a row with an infinite one
+      // becomes NaN whatever it is relative to), and scale 2^-e of a key as the
+      // sum of two f16 (the first in the low half).
       auto common = [&](float s) {
-        const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(s));
+        const unsigned top = __reduce_max_sync(0xffffffffu, s < INFINITY ? __float_as_uint(s) : 0u);
         return max(-36, (int)(top >> 23) - 127 - 6);
       };
       auto two_halves = [](float s, int e) {

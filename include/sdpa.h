@@ -400,11 +400,14 @@ typedef enum {
  * A cap's evaluation adds at most c * 2^-21 (c up to 128) or 2^-19 of the
  * capped score (above) to a score's error.
  * A row that sees no key (pos < 0) is zero, with lse = -inf.
- * A NaN in a query, or in a key it sees, makes its row and lse NaN.  A NaN or an
- * infinity in a value (or an infinite scale) reaches the rows that see it, and on
- * the tensor-core paths may reach rows of the same sequence that do not see that
- * token yet but are computed with one that does; rows of the cache that no new
- * row sees reach nothing.
+ * A NaN in a query, or a NaN or an infinite scale in a key it sees, makes its row
+ * and lse NaN and touches no other row.  A NaN, an infinity or an infinite scale
+ * in a value reaches the rows that see it, and on the tensor-core paths may reach
+ * rows of the same sequence that do not see that token yet but are computed with
+ * one that does; rows of the cache that no new row sees reach nothing.
+ * The tcgen05 path rounds 8-bit rows to f16 relative to the largest finite scale
+ * of 32 neighbouring keys: to 2^-11 of each number down to 2^-20 of what that
+ * scale stands for, to 2^-31 of that below.
  *   q, out   : [total_q, Hq, d], any token / head strides, dtype F32 (F32,
  *              E4M3, INT8 caches) or BF16 (BF16, E4M3, INT8 caches).  out
  *              must not overlap q or the cache.

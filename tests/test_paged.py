@@ -754,3 +754,33 @@ def test_values_that_are_not_finite(d, cdt, path, kv, n):
         spoil(j, math.nan)
     out, lse = run(window)
     assert torch.isfinite(out).all() and torch.equal(out, clean) and torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("path,kv,n", [("exact", [300, 90], [5, 2]), ("decode", [300, 90, 2500], [5, 1, 2]),
+                                       ("tcgen05", [300, 90], [200, 64]), ("tcgen05", [2500], [130])], ids=str)
+@pytest.mark.parametrize("cdt", [E4M3, INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_key_reaches_the_rows_that_see_it(d, cdt, path, kv, n):
+    """A key written with an infinity (its scale is infinite) makes NaN of the
+    rows that see it; those in front of it keep every bit."""
+    pool = R.Pool(cdt, 2, d, 16, kv, seed=4)
+    T = sum(n)
+    q = torch.randn(T, 4, d, generator=torch.Generator().manual_seed(5)).to(BF16).cuda()
+    cache, table, lens = pool.cache(), pool.table.cuda(), pool.lens.cuda()
+
+    def run():
+        lse = torch.empty(T, 4, device="cuda")
+        out = S.sdpa_paged(q, cache, table, lens, cu(n), max_q=max(n), lse=lse, path=path)
+        assert device_error() == 0
+        return out, lse
+
+    clean, clean_lse = run()
+    at = kv[0] - max(2, n[0] // 2)  # between the new rows
+    p, o = int(pool.table[0, at // 16]), at % 16
+    cache.k[p, 1, o] = 0
+    cache.k_scale[p, 1, o] = math.inf  # what cache_write makes of an infinity (an E4M3 one's own code is NaN)
+    bad = torch.zeros(T, 4, dtype=torch.bool, device="cuda")
+    bad[:n[0], 2:] = (torch.arange(n[0]) + kv[0] - n[0] >= at)[:, None].cuda()
+    out, lse = run()
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    assert torch.equal(out[~bad], clean[~bad]) and torch.equal(lse[~bad], clean_lse[~bad])
