@@ -784,3 +784,83 @@ def test_infinite_key_reaches_the_rows_that_see_it(d, cdt, path, kv, n):
     out, lse = run()
     assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
     assert torch.equal(out[~bad], clean[~bad]) and torch.equal(lse[~bad], clean_lse[~bad])
+
+
+@pytest.mark.parametrize("cdt", [BF16, INT8])
+def test_calls_follow_their_stream(cdt):
+    """Every operator called with ``stream=`` sees what was queued on that stream
+    in front of it: the inputs are filled there behind a long kernel."""
+    pool, q, k, v, table, lens = decode_setup(cdt)
+    new_q, new_k, new_v = (torch.randn_like(x) for x in (q, k, v))
+    new_lens = torch.tensor([650, 17, 64], dtype=torch.int32, device="cuda")
+
+    def steps(cache, q, k, v, lens, **kw):
+        S.cache_write(cache, k, v, table, lens, **kw)
+        return (S.sdpa_paged(q, cache, table, lens, **kw),) + S.cache_read(cache, table, lens, T=700, **kw)
+
+    want = steps(pool.cache(), new_q, new_k, new_v, new_lens)
+    old = steps(pool.cache(), q, k, v, lens)
+    assert all(not torch.equal(a, b) for a, b in zip(want, old))
+    cache, st = pool.cache(), torch.cuda.Stream()
+    busy = torch.zeros(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(40):
+            busy.add_(1)  # some milliseconds in all
+        for x, y in ((q, new_q), (k, new_k), (v, new_v), (lens, new_lens)):
+            x.copy_(y)
+    got = steps(cache, q, k, v, lens, stream=st)
+    assert not st.query(), "the stream was done before the calls: nothing was tested"
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and device_error() == 0
+
+
+@pytest.mark.parametrize("cdt", [BF16, E4M3])
+def test_decode_sequence_in_any_batch(cdt):
+    """One sequence beside different others: its keys are cut elsewhere each
+    time, its result stays within the bound."""
+    kv = [5000, 300, 2900, 1, 700, 64]
+    pool = R.Pool(cdt, 2, 128, 16, kv, seed=3)
+    q = torch.randn(6, 8, 128, generator=torch.Generator().manual_seed(4)).to(BF16)
+    codes = cdt == E4M3
+    want, wlse, tol, ltol = R.attend(pool, q, [1] * 6, u_p=R.U[torch.float16 if codes else BF16],
+                                     p_floor=2.0 ** -37 if codes else 0.0)
+    cache, bits_seen = pool.cache(), set()
+    for batch in ([0], [0, 1], [2, 0], [0, 1, 2, 3, 4, 5], [5, 4, 3, 2, 1, 0], [2] * 40 + [0] + [4] * 30, [0] * 7):
+        lse = torch.empty(len(batch), 8, device="cuda")
+        out = S.sdpa_paged(q[batch].cuda(), cache, pool.table[batch].cuda(), pool.lens[batch].cuda(), lse=lse, path="decode")
+        assert device_error() == 0
+        R.check(out, want[batch], tol[batch], BF16, f"{cdt} {batch}")
+        R.check_lse(lse, wlse[batch], ltol[batch], f"{cdt} {batch}")
+        bits_seen.add(lse[batch.index(0)].cpu().numpy().tobytes())
+    assert len(bits_seen) > 1, "every batch cut the sequence alike: nothing was tested"
+
+
+@pytest.mark.parametrize("cdt", [E4M3, INT8])
+def test_codes_of_every_scale(cdt):
+    """Rows whose scale has all ones in its significand, the one kind of divisor
+    whose reciprocal does not give the rounded quotient, and scales of every size."""
+    Q = R.QMAX[cdt]
+    s = torch.cat([torch.tensor([2.0 ** e], dtype=F32).view(torch.int32) - 1 for e in range(-29, 116)]).view(F32)
+    near = (s.double() * Q).float().view(torch.int32)[:, None] + torch.arange(-3, 4, dtype=torch.int32)
+    near = near.view(F32)
+    hit = (near.double() / Q).float() == s[:, None]  # the quotients of maxima that round to it
+    assert hit.any(1).all()
+    top = near[torch.arange(len(s)), hit.int().argmax(1)]
+    g = torch.Generator().manual_seed(3)
+    top = torch.cat([top, torch.exp(torch.empty(2000).uniform_(-60, 80, generator=g))])
+    d, T = 128, len(top)
+    x = torch.empty(T, 2, d).uniform_(-1, 1, generator=g) * top[:, None, None]
+    x[:, :, 5] = top[:, None]
+    # halfway between two codes and next to it
+    step = (x[:, 1, 6:40] / top[:, None] * Q).round() + 0.5
+    x[:, 1, 6:40] = (step.clamp(-Q + 0.5, Q - 0.5).double() / Q * top[:, None].double()).float()
+    cache = S.KVCache.empty(-(-T // 16), 16, 2, d, cdt)
+    table = torch.arange(-(-T // 16), dtype=torch.int32, device="cuda")[None]
+    S.cache_write(cache, x.cuda(), x.flip(1).cuda(), table, torch.tensor([T], dtype=torch.int32, device="cuda"), cu([T]))
+    assert device_error() == 0
+    c, want = R.quantise(x, cdt)
+    assert ((want.float().view(torch.int32) & 0x7fffff) == 0x7fffff).sum() >= 2 * len(s)
+    flat = lambda t: t.transpose(1, 2).flatten(0, 1)[:T].cpu()
+    for raw, sc, ref, refs in ((cache.k, cache.k_scale, c, want), (cache.v, cache.v_scale, c.flip(1), want.flip(1))):
+        assert torch.equal(flat(raw.float()).double(), ref) and torch.equal(flat(sc), refs.float())
