@@ -864,3 +864,98 @@ def test_codes_of_every_scale(cdt):
     flat = lambda t: t.transpose(1, 2).flatten(0, 1)[:T].cpu()
     for raw, sc, ref, refs in ((cache.k, cache.k_scale, c, want), (cache.v, cache.v_scale, c.flip(1), want.flip(1))):
         assert torch.equal(flat(raw.float()).double(), ref) and torch.equal(flat(sc), refs.float())
+
+
+@pytest.mark.parametrize("path", ["exact", "auto", "tcgen05"])
+@pytest.mark.parametrize("cdt", [BF16, INT8])
+def test_many_sequences_of_every_kind(cdt, path):
+    """More sequences than any block has threads, new rows from none to a chunk,
+    tables wider than their rows' pages and sliced from a wider tensor; rows of
+    nobody in front of the first sequence and behind the last keep out and lse."""
+    kv = [(i * 53) % 120 for i in range(1200)]
+    n = [0 if i % 4 == 0 else min(kv[i], 1 + (i * 7) % (90 if i % 100 == 3 else 5)) for i in range(1200)]
+    pool = R.Pool(cdt, 1, 64, 16, kv, seed=2)
+    front, T = 3, sum(n)
+    q = torch.randn(front + T + 4, 4, 64, generator=torch.Generator().manual_seed(3)).to(BF16)
+    wide = torch.full((1200, pool.table.shape[1] + 9), -3, dtype=torch.int32)
+    wide[:, 2:2 + pool.table.shape[1]] = pool.table
+    out = torch.full((front + T + 4, 4, 64), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((front + T + 4, 4), 7.0, device="cuda")
+    S.sdpa_paged(q.cuda(), pool.cache(), wide.cuda()[:, 2:-5], pool.lens.cuda(), cu(n) + front, max_q=max(n), out=out, lse=lse,
+                 path=path)
+    assert device_error() == 0
+    mine = slice(front, front + T)
+    codes = cdt in R.QMAX
+    want, wlse, tol, ltol = R.attend(pool, q[mine], n, u_p=0.0 if path == "exact" else R.U[torch.float16 if codes else BF16],
+                                     p_floor=2.0 ** -37 if path != "exact" and codes else 0.0,
+                                     u_kv=R.U[torch.float16] if path != "exact" and codes else 0.0)
+    R.check(out[mine], want, tol, BF16, f"{path} {cdt}")
+    R.check_lse(lse[mine], wlse, ltol, f"{path} {cdt}")
+    for t in (out, lse):
+        assert (t[:front] == 7).all() and (t[front + T:] == 7).all()
+
+
+@pytest.mark.parametrize("path", ["exact", "decode", "tcgen05"])
+def test_tables_without_pages(path):
+    """A batch whose table has no pages: every row sees nothing, and a write says so."""
+    cache = R.Pool(BF16, 2, 64, 16, [20]).cache()
+    table, lens = (torch.zeros(*s, dtype=torch.int32, device="cuda") for s in ((3, 0), (3,)))
+    lse = torch.zeros(6, 4, device="cuda")
+    out = S.sdpa_paged(torch.ones(6, 4, 64, dtype=BF16, device="cuda"), cache, table, lens, cu([1, 2, 3]), max_q=3, lse=lse, path=path)
+    assert device_error() == 0 and (out == 0).all() and (lse == -math.inf).all()
+    k, v = S.cache_read(cache, table, lens, T=5)
+    assert device_error() == 0 and (k == 0).all() and (v == 0).all()
+    x = torch.ones(3, 2, 64, dtype=BF16, device="cuda")
+    S.cache_write(cache, x, x, table, lens)
+    assert device_error() == -7
+
+
+@pytest.mark.parametrize("cdt", [F32, BF16, E4M3, INT8])
+def test_read_of_the_first_tokens(cdt):
+    """T below the sequences' lengths, odd, one, and past the longest."""
+    kv = [300, 0, 1, 77]
+    pool = R.Pool(cdt, 3, 64, 16, kv, seed=8)
+    io = F32 if cdt == F32 else BF16
+    cache, table, lens = pool.cache(), pool.table.cuda(), pool.lens.cuda()
+    for T in (1, 2, 33, 64, 77, 299, 300, 301):
+        got = S.cache_read(cache, table, lens, T=T)
+        assert device_error() == 0
+        for which, x in enumerate(got):
+            assert x.shape == (4, 3, T, 64) and x.dtype == io
+            for b, L in enumerate(kv):
+                m = min(L, T)
+                want = pool.tokens(which, b, m).float() if m else torch.zeros(3, 0, 64)
+                assert torch.equal(x[b, :, :m].cpu(), want.to(io)) and (x[b, :, m:] == 0).all()
+
+
+def test_threads_call_at_once():
+    """Several host threads, each with its stream, on one cache and on their own."""
+    import threading
+    sets = [decode_setup(BF16 if i % 2 else E4M3, 64, (2000 + 100 * i, 900, 64)) for i in range(4)]
+    caches = [s[0].cache() for s in sets]
+    chunks = [torch.randn(150, 8, 64, device="cuda").to(BF16) for _ in sets]
+    cuq = cu([100, 30, 20])
+    step = lambda i: (S.sdpa_paged(sets[i][1], caches[i], sets[i][4], sets[i][5]),
+                      S.sdpa_paged(chunks[i], caches[i], sets[i][4], sets[i][5], cuq, max_q=100))
+    want = [step(i) for i in range(4)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(t):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for j in range(30):
+                    i = (t + j) % 4 if j % 3 else 0  # one cache for all, or one each
+                    got = step(i)
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                        bad.append((t, j))
+        except Exception as e:  # reported by the main thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and device_error() == 0
