@@ -87,6 +87,13 @@ __device__ __forceinline__ constexpr bool dcheck_q(const Params&, long long, lon
 __device__ __forceinline__ constexpr bool dcheck_kv(const Params&, long long, long long, long long) { return true; }
 #endif
 
+// A load of what an earlier grid of the stream may have written: the rows and
+// scales another call leaves, lengths, tables.  That grid may still run when this
+// one starts (griddepcontrol), so the read-only path, __ldg, whose data must not
+// change while the grid lives, is not for it.
+template <typename T>
+__device__ __forceinline__ T ld_prior(const T* p) { return *p; }
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <typename T> __device__ __forceinline__ T from_f32(float x);

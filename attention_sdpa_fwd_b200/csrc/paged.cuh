@@ -58,13 +58,6 @@ struct Seq {
   int q0, n, L;
 };
 
-// A load of what an earlier grid of the stream may have written: the rows and
-// scales another call leaves, lengths, tables.  That grid may still run when this
-// one starts (griddepcontrol), so the read-only path, __ldg, whose data must not
-// change while the grid lives, is not for it.
-template <typename T>
-__device__ __forceinline__ T ld_prior(const T* p) { return *p; }
-
 __device__ __forceinline__ void index_error(int* err) {
   if (err != nullptr) atomicOr(err, ERR_INDEX);
 }

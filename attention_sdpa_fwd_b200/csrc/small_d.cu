@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kRowsPerCta, 7) small_d_kernel(Params p, int h
   const long long zq = (long long)b * p.Hq + h;
   const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + q_off(p, b, head_ok ? h : 0, valid ? i : 0);
   float q[D16];
-  bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(qrow)), q);
-  bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(qrow) + 1), q + 8);
+  bf16x8_to_f32(ld_prior(reinterpret_cast<const uint4*>(qrow)), q);
+  bf16x8_to_f32(ld_prior(reinterpret_cast<const uint4*>(qrow) + 1), q + 8);
   const float sl = p.scale * kLog2e;
 #pragma unroll
   for (int c = 0; c < D16; ++c) q[c] *= sl;
@@ -135,12 +135,12 @@ __global__ void __launch_bounds__(kRowsPerCta, 7) small_d_kernel(Params p, int h
     if (head_ok && r < n && dcheck_kv(p, b, hk, j0 + r)) {
       const long long j = j0 + r;
       float f[D16];
-      bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(kb + j * p.skt)), f);
-      bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(kb + j * p.skt) + 1), f + 8);
+      bf16x8_to_f32(ld_prior(reinterpret_cast<const uint4*>(kb + j * p.skt)), f);
+      bf16x8_to_f32(ld_prior(reinterpret_cast<const uint4*>(kb + j * p.skt) + 1), f + 8);
 #pragma unroll
       for (int c = 0; c < D16; c += 4) sk[threadIdx.x][c / 4] = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
-      bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(vb + j * p.svt)), f);
-      bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(vb + j * p.svt) + 1), f + 8);
+      bf16x8_to_f32(ld_prior(reinterpret_cast<const uint4*>(vb + j * p.svt)), f);
+      bf16x8_to_f32(ld_prior(reinterpret_cast<const uint4*>(vb + j * p.svt) + 1), f + 8);
 #pragma unroll
       for (int c = 0; c < D16; c += 4) sv[threadIdx.x][c / 4] = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
     }
@@ -422,8 +422,8 @@ __global__ void __launch_bounds__(kRowsPerCta, MASKED ? 4 : 6) small_d_mma_kerne
     uint4 a = make_uint4(0, 0, 0, 0), c = a;
     if (valid && dcheck_q(p, b, h, i)) {
       const uint4* qrow = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + q_off(p, b, h, i));
-      a = __ldg(qrow);
-      c = __ldg(qrow + 1);
+      a = ld_prior(qrow);
+      c = ld_prior(qrow + 1);
     }
     *reinterpret_cast<uint4*>(sq + sw32(tid, 0)) = a;
     *reinterpret_cast<uint4*>(sq + sw32(tid, 1)) = c;
@@ -480,10 +480,10 @@ __global__ void __launch_bounds__(kRowsPerCta, MASKED ? 4 : 6) small_d_mma_kerne
       if (head_ok && r < n && dcheck_kv(p, b, hk, j0 + r)) {
         const uint4* kr = reinterpret_cast<const uint4*>(kb + (j0 + r) * p.skt);
         const uint4* vr = reinterpret_cast<const uint4*>(vb + (j0 + r) * p.svt);
-        k0 = __ldg(kr);
-        k1 = __ldg(kr + 1);
-        v0 = __ldg(vr);
-        v1 = __ldg(vr + 1);
+        k0 = ld_prior(kr);
+        k1 = ld_prior(kr + 1);
+        v0 = ld_prior(vr);
+        v1 = ld_prior(vr + 1);
       }
       *reinterpret_cast<uint4*>(sk + sw32(tid, 0)) = k0;
       *reinterpret_cast<uint4*>(sk + sw32(tid, 1)) = k1;
@@ -618,10 +618,10 @@ __global__ void __launch_bounds__(kSplitThreads, 3) split_kv_kernel(SplitArgs a)
     if (tid < n && dcheck_kv(p, b, hk, j0 + tid)) {
       const uint4* kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + k_off(p, b, hk, j0 + tid));
       const uint4* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v) + v_off(p, b, hk, j0 + tid));
-      k0 = __ldg(kr);
-      k1 = __ldg(kr + 1);
-      v0 = __ldg(vr);
-      v1 = __ldg(vr + 1);
+      k0 = ld_prior(kr);
+      k1 = ld_prior(kr + 1);
+      v0 = ld_prior(vr);
+      v1 = ld_prior(vr + 1);
     }
     *reinterpret_cast<uint4*>(sk + sw32(tid, 0)) = k0;
     *reinterpret_cast<uint4*>(sk + sw32(tid, 1)) = k1;
@@ -636,8 +636,8 @@ __global__ void __launch_bounds__(kSplitThreads, 3) split_kv_kernel(SplitArgs a)
       uint4 q0 = make_uint4(0, 0, 0, 0), q1 = q0;
       if (rb + tid < p.Tq && dcheck_q(p, b, h, rb + tid)) {
         const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + q_off(p, b, h, rb + tid));
-        q0 = __ldg(qr);
-        q1 = __ldg(qr + 1);
+        q0 = ld_prior(qr);
+        q1 = ld_prior(qr + 1);
       }
       *reinterpret_cast<uint4*>(sq + sw32(tid, 0)) = q0;
       *reinterpret_cast<uint4*>(sq + sw32(tid, 1)) = q1;
@@ -779,16 +779,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kv_cluster_kernel(Clus
       if (tk < n && dcheck_kv(p, b, hk, j0 + tk)) {
         const uint4* kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + k_off(p, b, hk, j0 + tk));
         const uint4* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v) + v_off(p, b, hk, j0 + tk));
-        kv[u][0] = __ldg(kr);
-        kv[u][1] = __ldg(kr + 1);
-        kv[u][2] = __ldg(vr);
-        kv[u][3] = __ldg(vr + 1);
+        kv[u][0] = ld_prior(kr);
+        kv[u][1] = ld_prior(kr + 1);
+        kv[u][2] = ld_prior(vr);
+        kv[u][3] = ld_prior(vr + 1);
       }
     }
     if (tid < mrows && tid < p.Tq && dcheck_q(p, b, h, tid)) {
       const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + q_off(p, b, h, tid));
-      qv[0] = __ldg(qr);
-      qv[1] = __ldg(qr + 1);
+      qv[0] = ld_prior(qr);
+      qv[1] = ld_prior(qr + 1);
     }
 #pragma unroll
     for (int u = 0; u < KPT; ++u) {

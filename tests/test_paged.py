@@ -959,3 +959,36 @@ def test_threads_call_at_once():
     for t in threads:
         t.join()
     assert not bad and device_error() == 0
+
+
+@pytest.mark.parametrize("Tq,T", [(900, 20), (300, 200), (8, 2000)])
+def test_narrow_heads_read_back_for_dense_calls(Tq, T):
+    """Rows written, read back and attended densely at head_dim 16 with nothing
+    between the calls, each reading what the one before it wrote."""
+    cache = S.KVCache.empty(260, 16, 2, 16, BF16)
+    table = torch.randperm(260, generator=torch.Generator().manual_seed(1)).int().cuda()[:250].view(2, 125)
+    lens = torch.tensor([T, T], dtype=torch.int32, device="cuda")
+    rows = torch.randn(8, 2 * T, 2, 16, device="cuda").to(BF16)
+    q = torch.randn(2, 4, Tq, 16, device="cuda").to(BF16)
+    k_out, v_out = (torch.zeros(2, 2, T, 16, dtype=BF16, device="cuda") for _ in range(2))
+    x, y = torch.empty_like(q), torch.empty_like(q)
+
+    def steps(wait):
+        outs = []
+        for i in range(4):
+            S.cache_write(cache, rows[2 * i], rows[2 * i + 1], table, lens, cuq, max_q=T)
+            wait()
+            S.cache_read(cache, table, lens, k_out, v_out)
+            wait()
+            S.sdpa(q, k_out, v_out, out=x)
+            wait()
+            S.sdpa(x, k_out, v_out, out=y)
+            wait()
+            outs += [x.clone(), y.clone()]
+        return outs
+
+    cuq = cu([T, T])
+    want = steps(torch.cuda.synchronize)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(want, steps(lambda: None)))
+    assert device_error() == 0
