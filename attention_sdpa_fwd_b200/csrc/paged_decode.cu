@@ -36,7 +36,10 @@
 //     out = sum p_j code_j / sum p_j (1 / vs_j)
 // p_j is kept within 2^15 (f16) by m, which may lag 2^3 behind, and offset by
 // 2^12, so that a weight down to 2^-26 of the largest keeps f16's 11 bits and
-// none is off by more than 2^-37 of it; the sums are fp32.
+// none is off by more than 2^-37 of it; the sums are fp32.  Beside bf16 values the
+// weights are bf16 too (one mma takes both operands in one type, and bf16 values
+// do not fit f16): 2^-8 of a weight, which takes the error of a batch's outputs
+// from 1.7e-3, their own rounding, to 2.3e-3 of their size.
 #include <math.h>
 #include <string.h>
 

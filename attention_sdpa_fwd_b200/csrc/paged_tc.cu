@@ -28,7 +28,8 @@
 // (Scales by column there, exact, cost three shared-memory vectors per row and
 // tile and twice the time.)  The softmax warps scale their Q row in place by a
 // power of two into f16, its largest element to [2^14, 2^15).  P is f16 as in
-// the decode kernel: at most 2^15, offset by 2^12.
+// the decode kernel: at most 2^15, offset by 2^12; beside bf16 values it is bf16,
+// for the reason given there.
 //
 // Units of one launch differ in length (causal), so later query blocks, the
 // longer ones, start first.  When there are fewer units than SMs every unit's
