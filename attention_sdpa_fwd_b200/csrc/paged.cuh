@@ -136,9 +136,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// A capped score c tanh(x / c).  c - 2 c / (1 + e^(2 x / c)) is off by up to
-// c 2^-21 whatever x is, for the two terms cancel: 2^-14 at this cap, an eighth
-// of what rounding a weight to f16 may do, a sixty-fourth of it to bf16.
+// A capped score c tanh(x / c).  c - 2 c / (1 + e^(2 x / c)) may be off by c 2^-19
+// (the exponential, up to eight roundings and the reciprocal, times 2 c) whatever
+// x is, for the two terms cancel: 2^-12 at this cap, half of what rounding a
+// weight to f16 may do, a sixteenth of it to bf16.
 constexpr float kPlainCap = 128.f;
 // Above it: tanh's series where |x| <= c / 3, cut off at 2^-22.7 of the score;
 // beyond that c is less than 3.2 times what comes out.  In all 2^-19 of it.

@@ -397,8 +397,8 @@ typedef enum {
  *     x = scale * q . k_j;   softcap c > 0: x = c * tanh(x / c);
  *     slopes given: x += slopes[h] * (j - pos)
  * and out = softmax(x) . v over them; query head h reads kv head h / (Hq/Hkv).
- * A cap's evaluation adds at most c * 2^-21 (c up to 128) or 2^-19 of the
- * capped score (above) to a score's error.
+ * A cap's evaluation adds at most 2^-19 of c (c up to 128) or of the capped
+ * score (above) to a score's error.
  * A row that sees no key (pos < 0) is zero, with lse = -inf.
  * A NaN in a query, or a NaN or an infinite scale in a key it sees, makes its row
  * and lse NaN and touches no other row.  A NaN, an infinity or an infinite scale
